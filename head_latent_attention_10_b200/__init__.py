@@ -24,7 +24,8 @@ EXPORTED = ("mla_status_string", "mla_append_cache", "mla_append_latent", "mla_a
             "mla_decode_workspace_size", "mla_decode", "mla_decode_error", "mla_up_v",
             "mla_kernel_launches", "mla_decode_ctas", "mla_decode_noalloc",
             "mla_prefill_workspace_size", "mla_prefill", "mla_append_latent_fp8", "mla_decode_fp8",
-            "mla_fold_weights", "mla_absorb_q_folded", "mla_up_out_folded")
+            "mla_fold_weights", "mla_absorb_q_folded", "mla_up_out_folded", "mla_append_latent_int4",
+            "mla_gather_latent_int4", "mla_decode_int4", "mla_prefill_int4")
 
 
 class MLAError(RuntimeError):
@@ -88,6 +89,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mla_fold_weights.argtypes = [D, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp]
     lib.mla_absorb_q_folded.argtypes = [D, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp]
     lib.mla_up_out_folded.argtypes = [D, _vp, _i, _vp, _i, _vp, _vp]
+    lib.mla_append_latent_int4.argtypes = [D, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _vp, _vp, _i, _vp, _f, _vp, _vp]
+    lib.mla_gather_latent_int4.argtypes = [D, _vp, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _vp]
+    lib.mla_decode_int4.argtypes = [D, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, ctypes.c_size_t,
+                                    ctypes.c_uint32, _vp]
+    lib.mla_prefill_int4.argtypes = [D, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp,
+                                     _vp, ctypes.c_size_t, ctypes.c_uint32, _vp]
     lib.mla_kernel_launches.argtypes = []
     lib.mla_kernel_launches.restype = ctypes.c_uint64
     for name in EXPORTED:
@@ -108,10 +115,15 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _addr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
 def _stream(stream) -> Optional[int]:
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:   # the raw handle: building a Stream object costs more than the launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(status: int, where: str) -> None:
@@ -232,6 +244,98 @@ def mla_decode_fp8(d, q_abs, codes, scales, block_table, seq_lens, s, out_latent
         ctypes.byref(d), _ptr(q_abs), _ptr(codes), _ptr(scales), codes.shape[0], _ptr(block_table),
         block_table.shape[1], _ptr(seq_lens), B, s, _ptr(out_latent), _ptr(out_lse), _ptr(workspace),
         workspace.numel() * workspace.element_size(), flags, _stream(stream)), "mla_decode_fp8")
+
+
+def _tensors(where, *wanted) -> None:
+    """Raise ValueError unless every (name, tensor, dtype, shape) in `wanted` is
+    a contiguous tensor of that dtype and shape on the current GPU (whose
+    current stream the call runs on).  A tensor of None was left out by the
+    caller; the sizes given as -1 are free."""
+    import torch
+    places = {}
+    for name, t, dtype, shape in wanted:
+        if t is None:
+            continue
+        got = t.shape
+        if t.dtype is not dtype or (got != shape and (len(got) != len(shape) or
+                                                      any(n != m and n != -1 for n, m in zip(shape, got)))):
+            want = " x ".join("any" if n == -1 else str(n) for n in shape)
+            raise ValueError(f"{where}: {name} must be {dtype} of shape {want}, got {t.dtype} of {tuple(got)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+        places[t.get_device()] = name
+    for place, name in places.items():
+        if place < 0 or place != torch.cuda.current_device():
+            raise ValueError(f"{where}: {name} must live on the current GPU")
+
+
+def mla_append_latent_int4(d, c_kv, k_rope, seq_idx, pos, block_table, codes, scales, err_word=None,
+                           stream=None, kv_norm_weight=None, kv_norm_eps=1e-6):
+    """The row [c_kv | RoPE(k_rope, pos)] (RMS-normalised latent if
+    kv_norm_weight is given) quantized to 4-bit codes [num_blocks][64][288]
+    uint8 with a scale byte per 16 values, [num_blocks][64][36] uint8."""
+    import torch
+    T, nb = c_kv.shape[0], codes.shape[0]
+    _tensors("mla_append_latent_int4", ("c_kv", c_kv, torch.bfloat16, (T, 512)), ("k_rope", k_rope, torch.bfloat16, (T, 64)),
+             ("seq_idx", seq_idx, torch.int32, (T,)), ("pos", pos, torch.int32, (T,)),
+             ("block_table", block_table, torch.int32, (-1, -1)), ("codes", codes, torch.uint8, (nb, 64, 288)),
+             ("scales", scales, torch.uint8, (nb, 64, 36)), ("kv_norm_weight", kv_norm_weight, torch.bfloat16, (512,)),
+             ("err_word", err_word, torch.int32, (1,)))
+    _check(load_library().mla_append_latent_int4(
+        ctypes.byref(d), c_kv.data_ptr(), k_rope.data_ptr(), T, seq_idx.data_ptr(), pos.data_ptr(),
+        block_table.data_ptr(), block_table.shape[0], block_table.shape[1], codes.data_ptr(), scales.data_ptr(), nb,
+        _addr(kv_norm_weight), kv_norm_eps, _addr(err_word), _stream(stream)), "mla_append_latent_int4")
+
+
+def mla_gather_latent_int4(d, codes, scales, seq_idx, pos, block_table, rows, err_word=None, stream=None):
+    """rows[t] = the bf16 values of the 4-bit row of (seq_idx[t], pos[t])."""
+    import torch
+    T, nb = seq_idx.shape[0], codes.shape[0]
+    _tensors("mla_gather_latent_int4", ("seq_idx", seq_idx, torch.int32, (T,)), ("pos", pos, torch.int32, (T,)),
+             ("block_table", block_table, torch.int32, (-1, -1)), ("rows", rows, torch.bfloat16, (T, 576)),
+             ("codes", codes, torch.uint8, (nb, 64, 288)), ("scales", scales, torch.uint8, (nb, 64, 36)),
+             ("err_word", err_word, torch.int32, (1,)))
+    _check(load_library().mla_gather_latent_int4(
+        ctypes.byref(d), codes.data_ptr(), scales.data_ptr(), nb, seq_idx.data_ptr(), pos.data_ptr(), T,
+        block_table.data_ptr(), block_table.shape[0], block_table.shape[1], rows.data_ptr(), _addr(err_word),
+        _stream(stream)), "mla_gather_latent_int4")
+
+
+def mla_decode_int4(d, q_abs, codes, scales, block_table, seq_lens, s, out_latent, out_lse, workspace,
+                    flags: int = 0, stream=None):
+    """Absorbed attention over the 4-bit latent cache; writes out_latent and
+    out_lse.  workspace: a uint8 tensor of mla_decode_workspace_size bytes."""
+    import torch
+    B, H, nb, mb = seq_lens.shape[0], d.num_heads, codes.shape[0], block_table.shape[-1]
+    _tensors("mla_decode_int4", ("q_abs", q_abs, torch.bfloat16, (B * s, H, 576)), ("seq_lens", seq_lens, torch.int32, (B,)),
+             ("block_table", block_table, torch.int32, (B, mb)), ("out_latent", out_latent, torch.bfloat16, (B * s, H, 512)),
+             ("out_lse", out_lse, torch.float32, (B * s, H)), ("codes", codes, torch.uint8, (nb, 64, 288)),
+             ("scales", scales, torch.uint8, (nb, 64, 36)), ("workspace", workspace, torch.uint8, (-1,)))
+    _check(load_library().mla_decode_int4(
+        ctypes.byref(d), q_abs.data_ptr(), codes.data_ptr(), scales.data_ptr(), nb, block_table.data_ptr(), mb,
+        seq_lens.data_ptr(), B, s, out_latent.data_ptr(), _addr(out_lse), workspace.data_ptr(), workspace.numel(),
+        flags, _stream(stream)), "mla_decode_int4")
+
+
+def mla_prefill_int4(d, q_nope, q_rope, q_pos, w_uk, w_uv, codes, scales, block_table, seq_lens, s, max_seq_len,
+                     out, out_lse, workspace, flags: int = 0, stream=None):
+    """Expanded-form attention of the last s tokens of each sequence over its
+    4-bit cached latents; writes the per-head outputs out [B*s][H][128].
+    workspace: a uint8 tensor of mla_prefill_workspace_size bytes."""
+    import torch
+    B, H, nb, mb = seq_lens.shape[0], d.num_heads, codes.shape[0], block_table.shape[-1]
+    _tensors("mla_prefill_int4", ("q_nope", q_nope, torch.bfloat16, (B * s, H, 128)),
+             ("q_rope", q_rope, torch.bfloat16, (B * s, H, 64)), ("q_pos", q_pos, torch.int32, (B * s,)),
+             ("w_uk", w_uk, torch.bfloat16, (H, 128, 512)), ("w_uv", w_uv, torch.bfloat16, (H, 128, 512)),
+             ("block_table", block_table, torch.int32, (B, mb)), ("seq_lens", seq_lens, torch.int32, (B,)),
+             ("out", out, torch.bfloat16, (B * s, H, 128)), ("out_lse", out_lse, torch.float32, (B * s, H)),
+             ("codes", codes, torch.uint8, (nb, 64, 288)), ("scales", scales, torch.uint8, (nb, 64, 36)),
+             ("workspace", workspace, torch.uint8, (-1,)))
+    _check(load_library().mla_prefill_int4(
+        ctypes.byref(d), q_nope.data_ptr(), q_rope.data_ptr(), _addr(q_pos), w_uk.data_ptr(), w_uv.data_ptr(),
+        codes.data_ptr(), scales.data_ptr(), nb, block_table.data_ptr(), mb, seq_lens.data_ptr(), B, s, max_seq_len,
+        out.data_ptr(), _addr(out_lse), workspace.data_ptr(), workspace.numel(), flags, _stream(stream)),
+        "mla_prefill_int4")
 
 
 def mla_fold_weights(d, w_uq=None, w_uk=None, w_qk=None, w_o=None, w_uv=None, w_ov=None, stream=None):

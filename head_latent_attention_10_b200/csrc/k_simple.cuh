@@ -135,21 +135,33 @@ latent_rmsnorm_kernel(int T, const int32_t *__restrict__ seq_idx, const int32_t 
     row[lane + 32] = v1;
 }
 
+// Rows of the bf16 cache as 16-byte units of 8 values: unit c of the row in
+// physical slot `slot` holds columns [8c, 8c + 8).
+struct Bf16Rows {
+    const bf16 *cache;
+    __device__ __forceinline__ uint4 unit(long long slot, int c) const
+    {
+        return reinterpret_cast<const uint4 *>(cache + slot * kRow)[c];
+    }
+};
+
 // ------------------------------------------------------------- simple decode
 // One CTA per (query row, group of 8 heads, KV split of kSimpleSplit tokens).
 // 32-token tiles are staged in shared memory; warp w scores head w against
 // the tile (one token per lane) and keeps its online-softmax state; every
 // thread then accumulates two latent columns of all 8 heads.  Each split
-// writes a normalized partial latent and its log2-sum-exp.
+// writes a normalized partial latent and its log2-sum-exp.  Rows: how the
+// cache's rows are read as bf16 (Bf16Rows, Int4Rows).
 constexpr int kSimpleHeads = 8;
 constexpr int kSimpleTile = 32;
 constexpr int kSimpleSplit = 1024;
 constexpr int kSimpleRowPad = kRow + 8;  // 1168-byte stride: 16-B reads hit distinct banks
 constexpr int kSimpleSmem = kSimpleHeads * kRow * sizeof(float) + kSimpleTile * kSimpleRowPad * sizeof(bf16);
 
+template <class Rows>
 __global__ void __launch_bounds__(256)
-decode_simple_kernel(const bf16 *__restrict__ q_abs, const bf16 *__restrict__ cache,
-                     int num_blocks, const int32_t *__restrict__ block_table, int max_blocks,
+decode_simple_kernel(const bf16 *__restrict__ q_abs, const Rows cache, int num_blocks,
+                     const int32_t *__restrict__ block_table, int max_blocks,
                      const int32_t *__restrict__ seq_lens, int s, int H, float scale_log2,
                      float *__restrict__ part_o, float *__restrict__ part_lse2, int nsplit_max,
                      uint32_t *err)
@@ -193,7 +205,7 @@ decode_simple_kernel(const bf16 *__restrict__ q_abs, const bf16 *__restrict__ ca
             if (j < j1) {
                 const int blk = block_table[(long long)b * max_blocks + j / kBlock];
                 if (blk >= 0 && blk < num_blocks) {
-                    v = reinterpret_cast<const uint4 *>(cache + ((long long)blk * kBlock + j % kBlock) * kRow)[ch];
+                    v = cache.unit((long long)blk * kBlock + j % kBlock, ch);
                     ok = 1;
                 } else if (ch == 0) {
                     set_error(err, MLA_DEVERR_BLOCK_ID);

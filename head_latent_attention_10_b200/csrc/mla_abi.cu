@@ -12,6 +12,7 @@
 #include "absorb.cuh"
 #include "append_proj.cuh"
 #include "common.cuh"
+#include "int4.cuh"
 #include "k_simple.cuh"
 #include "tc_decode64.cuh"
 #include "tc_gemm.cuh"
@@ -339,6 +340,126 @@ mla_status_t run_tc_decode(const mla_dims_t *dims, const void *q_abs, const void
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
+// The CUDA-core decode (MLA_FORCE_SIMPLE) over rows read through `rows`.
+template <class Rows>
+mla_status_t run_simple_decode(const mla_dims_t *dims, const void *q_abs, const Rows &rows, int num_blocks,
+                               const int32_t *block_table, int max_blocks, const int32_t *seq_lens, int B, int s,
+                               void *out_latent, float *out_lse, char *ws, size_t ws_bytes, cudaStream_t strm)
+{
+    const int H = dims->num_heads, T = B * s;
+    uint32_t *err = (uint32_t *)ws;
+    const SimpleWs w = simple_ws(H, T, max_blocks * kBlock);
+    if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
+    if (cudaMemsetAsync(err, 0, sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
+    float *po = (float *)(ws + w.off_o);
+    float *pl = (float *)(ws + w.off_lse);
+    dim3 grid(T, H / kSimpleHeads, w.nsplit);
+    static std::atomic<bool> attr_set[kMaxDevices];
+    if (ensure_smem_attr(decode_simple_kernel<Rows>, kSimpleSmem, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
+    decode_simple_kernel<Rows><<<grid, 256, kSimpleSmem, strm>>>((const bf16 *)q_abs, rows, num_blocks, block_table,
+                                                                 max_blocks, seq_lens, s, H,
+                                                                 softmax_scale(dims) * kLog2e, po, pl, w.nsplit, err);
+    count_launch();
+    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    combine_simple_kernel<<<dim3(T, H), 128, 0, strm>>>(po, pl, w.nsplit, kSimpleSplit, seq_lens, max_blocks, s, H,
+                                                        (bf16 *)out_latent, out_lse, err);
+    count_launch();
+    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    return MLA_OK;
+}
+
+// The prefill over cache rows read through `cache` (argument checks are the
+// caller's).
+template <class Rows>
+mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void *q_rope, const int32_t *q_pos,
+                         const void *w_uk, const void *w_uv, const Rows &cache, int num_blocks,
+                         const int32_t *block_table, int max_blocks, const int32_t *seq_lens, int B, int s,
+                         int max_seq_len, void *out, float *out_lse, void *workspace, size_t ws_bytes, uint32_t flags,
+                         cudaStream_t strm)
+{
+    const int H = dims->num_heads;
+    const PfWs w = pf_ws(H, B, s, max_seq_len);
+    if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
+    const long long rows_total = (long long)B * w.lpad;
+    if (rows_total > (1ll << 31) - 1 || (long long)B * s * H > (1ll << 31) - 1) return MLA_ERR_UNSUPPORTED;
+    const int M = (int)rows_total;
+    char *ws = (char *)workspace;
+    uint32_t *err = (uint32_t *)ws;
+    bf16 *rows = (bf16 *)(ws + w.off_rows), *q_rot = (bf16 *)(ws + w.off_qr);
+    bf16 *kc = (bf16 *)(ws + w.off_kc), *vc = (bf16 *)(ws + w.off_vc);
+    const long long cap_blocks = (long long)max_blocks * kBlock;
+    const int l_cap = cap_blocks < max_seq_len ? (int)cap_blocks : max_seq_len;
+
+    // tensor maps: the expansions, one GEMM each over all heads,
+    // K^C [M][H*128] = rows [M][512] . [U^K_0; ..; U^K_{H-1}]^T (the stacked
+    // [H*128][512] weights are K-major as stored), and the attention
+    CUtensorMap ma, muk, muv, mkc, mvc, skc, svc;
+    if (!tmap(&ma, rows, kDc, M, 1, kRow, 0, 64, 128) ||
+        !tmap(&muk, w_uk, kDc, (uint64_t)H * kDh, 1, kDc, 0, 64, 256) ||
+        !tmap(&muv, w_uv, kDc, (uint64_t)H * kDh, 1, kDc, 0, 64, 256) ||
+        !make_tmap_3d(&skc, kc, (uint64_t)H * kDh, 1, M, (uint64_t)H * kDh * 2, (uint64_t)H * kDh * 2, 64, 1, 128,
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tmap_3d(&svc, vc, (uint64_t)H * kDh, 1, M, (uint64_t)H * kDh * 2, (uint64_t)H * kDh * 2, 64, 1, 128,
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tmap_3d(&mkc, kc, kDh, H, M, kDh * 2, (uint64_t)H * kDh * 2, 64, 1, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tmap_3d(&mvc, vc, kDh, H, M, kDh * 2, (uint64_t)H * kDh * 2, 64, 1, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+        return MLA_ERR_CUDA;
+    PrefillMaps pm;
+    {
+        const uint64_t odims[4] = {(uint64_t)kDh, (uint64_t)H, (uint64_t)s, (uint64_t)B};
+        const uint64_t ostr[3] = {(uint64_t)kDh * 2, (uint64_t)H * kDh * 2, (uint64_t)s * H * kDh * 2};
+        const uint32_t obox[4] = {64, 1, 128, 1};
+        if (!make_tmap_4d(&pm.out, out, odims, ostr, obox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !make_tmap_3d(&pm.kr, rows, kRow, M, 1, kRow * 2, (uint64_t)M * kRow * 2, 64, 128, 1,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+            return MLA_ERR_CUDA;
+        pm.kc = mkc;
+        pm.vc = mvc;
+    }
+    if (cudaMemsetAsync(err, 0, sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
+    {
+        const long long work = rows_total * (kRow / 8) + (long long)B * s * (kDr / 2);
+        long long blocks = (work + 255) / 256;
+        if (blocks > 8ll * sm_count()) blocks = 8ll * sm_count();
+        prefill_prepare_kernel<Rows><<<(int)blocks, 256, 0, strm>>>(cache, num_blocks, block_table, max_blocks,
+                                                                    seq_lens, B, s, H, w.lpad, l_cap, rows,
+                                                                    (const bf16 *)q_rope, q_pos, q_rot,
+                                                                    rope_table(dims), err);
+        count_launch();
+        if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    }
+    if (launch_tc_gemm<256, false, TcEpiTmaStore>(ma, muk, M, H * kDh, kDc, 1, TcEpiTmaStore{}, err, strm, &skc) !=
+            cudaSuccess ||
+        launch_tc_gemm<256, false, TcEpiTmaStore>(ma, muv, M, H * kDh, kDc, 1, TcEpiTmaStore{}, err, strm, &svc) !=
+            cudaSuccess)
+        return MLA_ERR_CUDA;
+    PrefillArgs pa;
+    pa.q_nope = (const bf16 *)q_nope;
+    pa.q_rot = q_rot;
+    pa.seq_lens = seq_lens;
+    pa.s = s;
+    pa.H = H;
+    pa.lpad = w.lpad;
+    pa.l_cap = l_cap;
+    pa.scale_log2 = softmax_scale(dims) * kLog2e;
+    pa.out_lse = out_lse;
+    pa.err = err;
+    pa.limit_ns = kWaitLimitNs;
+    static std::atomic<bool> attr_set[kMaxDevices];
+    if (ensure_smem_attr(tc_prefill_kernel, kPfSmem, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
+    tc_prefill_kernel<<<dim3((s + 127) / 128, H, B), kPfThreads, kPfSmem, strm>>>(pm, pa);
+    count_launch();
+    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    if (flags & MLA_SYNC_CHECK) {
+        uint32_t h = 0;
+        if (cudaMemcpyAsync(&h, err, sizeof h, cudaMemcpyDeviceToHost, strm) != cudaSuccess ||
+            cudaStreamSynchronize(strm) != cudaSuccess)
+            return MLA_ERR_CUDA;
+        if (h) return MLA_ERR_DEVICE;
+    }
+    return MLA_OK;
+}
+
 // Decode scratch for callers that pass no workspace: one array per device,
 // its address looked up once per device.
 __device__ __align__(256) unsigned char g_noalloc_scratch[MLA_NOALLOC_SCRATCH_BYTES];
@@ -386,6 +507,14 @@ mla_status_t append_project(const mla_dims_t *dims, const void *h, int T, int d_
     TcEpiAppend e2{(bf16 *)cache, seq_idx, pos, block_table, num_seqs, max_blocks, num_blocks, kDc, 1,
                    rope_table(dims), nullptr};
     return cuda_status(launch_tc_gemm<64, false>(ma, mb2, T, kDr, d_model, 1, e2, err_word, s));
+}
+
+// Sizes whose products stay within the 32-bit indexes that the kernels of the
+// 4-bit cache keep (rows, positions); larger ones are MLA_ERR_UNSUPPORTED.
+bool int4_sizes_ok(long long B, long long s, long long H, long long max_blocks)
+{
+    const long long top = (1ll << 31) - 1;
+    return max_blocks * kBlock <= top && B * s <= top && s * H <= top && B * s * H <= top;
 }
 
 }  // namespace
@@ -513,29 +642,13 @@ mla_status_t mla_decode(const mla_dims_t *dims, const void *q_abs, const void *c
     if (!q_abs || !cache || !block_table || !seq_lens || !out_latent) return MLA_ERR_INVALID_ARG;
     if (!aligned16(q_abs) || !aligned16(cache) || !aligned16(out_latent)) return MLA_ERR_INVALID_ARG;
     if (!workspace) return MLA_ERR_WORKSPACE;
-    const int H = dims->num_heads, T = B * s;
     cudaStream_t strm = as_stream(stream);
     char *ws = (char *)workspace;
     uint32_t *err = (uint32_t *)ws;
-    const float scale_log2 = softmax_scale(dims) * kLog2e;
     if (flags & MLA_FORCE_SIMPLE) {
-        const SimpleWs w = simple_ws(H, T, max_blocks * kBlock);
-        if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
-        if (cudaMemsetAsync(err, 0, sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
-        float *po = (float *)(ws + w.off_o);
-        float *pl = (float *)(ws + w.off_lse);
-        dim3 grid(T, H / kSimpleHeads, w.nsplit);
-        static std::atomic<bool> attr_set[kMaxDevices];
-        if (ensure_smem_attr(decode_simple_kernel, kSimpleSmem, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
-        decode_simple_kernel<<<grid, 256, kSimpleSmem, strm>>>((const bf16 *)q_abs, (const bf16 *)cache,
-                                                               num_blocks, block_table, max_blocks, seq_lens, s,
-                                                               H, scale_log2, po, pl, w.nsplit, err);
-        count_launch();
-        if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-        combine_simple_kernel<<<dim3(T, H), 128, 0, strm>>>(po, pl, w.nsplit, kSimpleSplit, seq_lens,
-                                                            max_blocks, s, H, (bf16 *)out_latent, out_lse, err);
-        count_launch();
-        if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+        const mla_status_t r = run_simple_decode(dims, q_abs, Bf16Rows{(const bf16 *)cache}, num_blocks, block_table,
+                                                 max_blocks, seq_lens, B, s, out_latent, out_lse, ws, ws_bytes, strm);
+        if (r != MLA_OK) return r;
     } else {
         const mla_status_t r = run_tc_decode<false>(dims, q_abs, cache, nullptr, num_blocks, block_table, max_blocks,
                                                     seq_lens, B, s, out_latent, out_lse, ws, ws_bytes, flags, strm);
@@ -640,88 +753,9 @@ mla_status_t mla_prefill(const mla_dims_t *dims, const void *q_nope, const void 
         !aligned16(out))
         return MLA_ERR_INVALID_ARG;
     if (!workspace) return MLA_ERR_WORKSPACE;
-    const int H = dims->num_heads;
-    const PfWs w = pf_ws(H, B, s, max_seq_len);
-    if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
-    const long long rows_total = (long long)B * w.lpad;
-    if (rows_total > (1ll << 31) - 1 || (long long)B * s * H > (1ll << 31) - 1) return MLA_ERR_UNSUPPORTED;
-    const int M = (int)rows_total;
-    cudaStream_t strm = as_stream(stream);
-    char *ws = (char *)workspace;
-    uint32_t *err = (uint32_t *)ws;
-    bf16 *rows = (bf16 *)(ws + w.off_rows), *q_rot = (bf16 *)(ws + w.off_qr);
-    bf16 *kc = (bf16 *)(ws + w.off_kc), *vc = (bf16 *)(ws + w.off_vc);
-    const long long cap_blocks = (long long)max_blocks * kBlock;
-    const int l_cap = cap_blocks < max_seq_len ? (int)cap_blocks : max_seq_len;
-
-    // tensor maps: the expansions, one GEMM each over all heads,
-    // K^C [M][H*128] = rows [M][512] . [U^K_0; ..; U^K_{H-1}]^T (the stacked
-    // [H*128][512] weights are K-major as stored), and the attention
-    CUtensorMap ma, muk, muv, mkc, mvc, skc, svc;
-    if (!tmap(&ma, rows, kDc, M, 1, kRow, 0, 64, 128) ||
-        !tmap(&muk, w_uk, kDc, (uint64_t)H * kDh, 1, kDc, 0, 64, 256) ||
-        !tmap(&muv, w_uv, kDc, (uint64_t)H * kDh, 1, kDc, 0, 64, 256) ||
-        !make_tmap_3d(&skc, kc, (uint64_t)H * kDh, 1, M, (uint64_t)H * kDh * 2, (uint64_t)H * kDh * 2, 64, 1, 128,
-                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tmap_3d(&svc, vc, (uint64_t)H * kDh, 1, M, (uint64_t)H * kDh * 2, (uint64_t)H * kDh * 2, 64, 1, 128,
-                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tmap_3d(&mkc, kc, kDh, H, M, kDh * 2, (uint64_t)H * kDh * 2, 64, 1, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tmap_3d(&mvc, vc, kDh, H, M, kDh * 2, (uint64_t)H * kDh * 2, 64, 1, 128, CU_TENSOR_MAP_SWIZZLE_128B))
-        return MLA_ERR_CUDA;
-    PrefillMaps pm;
-    {
-        const uint64_t odims[4] = {(uint64_t)kDh, (uint64_t)H, (uint64_t)s, (uint64_t)B};
-        const uint64_t ostr[3] = {(uint64_t)kDh * 2, (uint64_t)H * kDh * 2, (uint64_t)s * H * kDh * 2};
-        const uint32_t obox[4] = {64, 1, 128, 1};
-        if (!make_tmap_4d(&pm.out, out, odims, ostr, obox, CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !make_tmap_3d(&pm.kr, rows, kRow, M, 1, kRow * 2, (uint64_t)M * kRow * 2, 64, 128, 1,
-                          CU_TENSOR_MAP_SWIZZLE_128B))
-            return MLA_ERR_CUDA;
-        pm.kc = mkc;
-        pm.vc = mvc;
-    }
-    if (cudaMemsetAsync(err, 0, sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
-    {
-        const long long work = rows_total * (kRow / 8) + (long long)B * s * (kDr / 2);
-        long long blocks = (work + 255) / 256;
-        if (blocks > 8ll * sm_count()) blocks = 8ll * sm_count();
-        prefill_prepare_kernel<<<(int)blocks, 256, 0, strm>>>((const bf16 *)cache, num_blocks, block_table,
-                                                              max_blocks, seq_lens, B, s, H, w.lpad, l_cap, rows,
-                                                              (const bf16 *)q_rope, q_pos, q_rot, rope_table(dims),
-                                                              err);
-        count_launch();
-        if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-    }
-    if (launch_tc_gemm<256, false, TcEpiTmaStore>(ma, muk, M, H * kDh, kDc, 1, TcEpiTmaStore{}, err, strm, &skc) !=
-            cudaSuccess ||
-        launch_tc_gemm<256, false, TcEpiTmaStore>(ma, muv, M, H * kDh, kDc, 1, TcEpiTmaStore{}, err, strm, &svc) !=
-            cudaSuccess)
-        return MLA_ERR_CUDA;
-    PrefillArgs pa;
-    pa.q_nope = (const bf16 *)q_nope;
-    pa.q_rot = q_rot;
-    pa.seq_lens = seq_lens;
-    pa.s = s;
-    pa.H = H;
-    pa.lpad = w.lpad;
-    pa.l_cap = l_cap;
-    pa.scale_log2 = softmax_scale(dims) * kLog2e;
-    pa.out_lse = out_lse;
-    pa.err = err;
-    pa.limit_ns = kWaitLimitNs;
-    static std::atomic<bool> attr_set[kMaxDevices];
-    if (ensure_smem_attr(tc_prefill_kernel, kPfSmem, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
-    tc_prefill_kernel<<<dim3((s + 127) / 128, H, B), kPfThreads, kPfSmem, strm>>>(pm, pa);
-    count_launch();
-    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-    if (flags & MLA_SYNC_CHECK) {
-        uint32_t h = 0;
-        if (cudaMemcpyAsync(&h, err, sizeof h, cudaMemcpyDeviceToHost, strm) != cudaSuccess ||
-            cudaStreamSynchronize(strm) != cudaSuccess)
-            return MLA_ERR_CUDA;
-        if (h) return MLA_ERR_DEVICE;
-    }
-    return MLA_OK;
+    return run_prefill(dims, q_nope, q_rope, q_pos, w_uk, w_uv, Bf16Rows{(const bf16 *)cache}, num_blocks, block_table,
+                       max_blocks, seq_lens, B, s, max_seq_len, out, out_lse, workspace, ws_bytes, flags,
+                       as_stream(stream));
 }
 
 mla_status_t mla_append_latent_fp8(const mla_dims_t *dims, const void *c_kv, const void *k_rope, int T,
@@ -774,6 +808,106 @@ mla_status_t mla_decode_fp8(const mla_dims_t *dims, const void *q_abs, const voi
         if (host) return MLA_ERR_DEVICE;
     }
     return MLA_OK;
+}
+
+mla_status_t mla_append_latent_int4(const mla_dims_t *dims, const void *c_kv, const void *k_rope, int T,
+                                    const int32_t *seq_idx, const int32_t *pos, const int32_t *block_table,
+                                    int num_seqs, int max_blocks, void *codes, void *scales, int num_blocks,
+                                    const void *kv_norm_weight, float kv_norm_eps, uint32_t *err_word, void *stream)
+{
+    mla_status_t st = check_dims(dims);
+    if (st != MLA_OK) return st;
+    if (T < 0 || num_seqs < 0 || max_blocks < 0 || num_blocks < 0) return MLA_ERR_INVALID_ARG;
+    if (T == 0) return MLA_OK;
+    if (!c_kv || !k_rope || !seq_idx || !pos || !block_table || !codes || !scales) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(c_kv) || !aligned16(codes) || !aligned16(scales) || ((uintptr_t)k_rope & 3u))
+        return MLA_ERR_INVALID_ARG;
+    if (kv_norm_weight && (!aligned16(kv_norm_weight) || !(kv_norm_eps >= 0.f))) return MLA_ERR_INVALID_ARG;
+    if (!int4_sizes_ok(1, 1, 1, max_blocks) || T > (1 << 26)) return MLA_ERR_UNSUPPORTED;
+    append_latent_int4_kernel<<<(T + 7) / 8, 256, 0, as_stream(stream)>>>(
+        (const bf16 *)c_kv, (const bf16 *)k_rope, T, seq_idx, pos, block_table, num_seqs, max_blocks, (uint8_t *)codes,
+        (uint8_t *)scales, num_blocks, rope_table(dims), (const bf16 *)kv_norm_weight, kv_norm_eps, err_word);
+    count_launch();
+    return cuda_status(cudaGetLastError());
+}
+
+mla_status_t mla_gather_latent_int4(const mla_dims_t *dims, const void *codes, const void *scales, int num_blocks,
+                                    const int32_t *seq_idx, const int32_t *pos, int T, const int32_t *block_table,
+                                    int num_seqs, int max_blocks, void *rows, uint32_t *err_word, void *stream)
+{
+    mla_status_t st = check_dims(dims);
+    if (st != MLA_OK) return st;
+    if (T < 0 || num_seqs < 0 || max_blocks < 0 || num_blocks < 0) return MLA_ERR_INVALID_ARG;
+    if (T == 0) return MLA_OK;
+    if (!codes || !scales || !seq_idx || !pos || !block_table || !rows) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(rows)) return MLA_ERR_INVALID_ARG;
+    if (!int4_sizes_ok(1, 1, 1, max_blocks)) return MLA_ERR_UNSUPPORTED;
+    const int sms = sm_count();
+    if (sms <= 0) return MLA_ERR_CUDA;
+    long long blocks = ((long long)T * (kRow / 8) + 255) / 256;
+    if (blocks > 8ll * sms) blocks = 8ll * sms;
+    gather_latent_int4_kernel<<<(int)blocks, 256, 0, as_stream(stream)>>>(
+        Int4Rows{(const uint8_t *)codes, (const uint8_t *)scales}, num_blocks, seq_idx, pos, T, block_table, num_seqs,
+        max_blocks, (bf16 *)rows, err_word);
+    count_launch();
+    return cuda_status(cudaGetLastError());
+}
+
+mla_status_t mla_decode_int4(const mla_dims_t *dims, const void *q_abs, const void *codes, const void *scales,
+                             int num_blocks, const int32_t *block_table, int max_blocks, const int32_t *seq_lens,
+                             int B, int s, void *out_latent, float *out_lse, void *workspace, size_t ws_bytes,
+                             uint32_t flags, void *stream)
+{
+    mla_status_t st = check_dims(dims);
+    if (st != MLA_OK) return st;
+    if (B < 0 || s <= 0 || num_blocks < 0 || max_blocks < 0) return MLA_ERR_INVALID_ARG;
+    if (B == 0) return MLA_OK;
+    if (num_blocks == 0 || max_blocks == 0) return MLA_ERR_INVALID_ARG;
+    if (!q_abs || !codes || !scales || !block_table || !seq_lens || !out_latent) return MLA_ERR_INVALID_ARG;
+    if (!aligned16(q_abs) || !aligned16(codes) || !aligned16(scales) || !aligned16(out_latent))
+        return MLA_ERR_INVALID_ARG;
+    if (!int4_sizes_ok(B, s, dims->num_heads, max_blocks)) return MLA_ERR_UNSUPPORTED;
+    if (!workspace) return MLA_ERR_WORKSPACE;
+    cudaStream_t strm = as_stream(stream);
+    char *ws = (char *)workspace;
+    const mla_status_t r =
+        run_simple_decode(dims, q_abs, Int4Rows{(const uint8_t *)codes, (const uint8_t *)scales}, num_blocks,
+                          block_table, max_blocks, seq_lens, B, s, out_latent, out_lse, ws, ws_bytes, strm);
+    if (r != MLA_OK) return r;
+    if (flags & MLA_SYNC_CHECK) {
+        uint32_t host = 0;
+        if (cudaMemcpyAsync(&host, ws, sizeof host, cudaMemcpyDeviceToHost, strm) != cudaSuccess ||
+            cudaStreamSynchronize(strm) != cudaSuccess)
+            return MLA_ERR_CUDA;
+        if (host) return MLA_ERR_DEVICE;
+    }
+    return MLA_OK;
+}
+
+mla_status_t mla_prefill_int4(const mla_dims_t *dims, const void *q_nope, const void *q_rope, const int32_t *q_pos,
+                              const void *w_uk, const void *w_uv, const void *codes, const void *scales,
+                              int num_blocks, const int32_t *block_table, int max_blocks, const int32_t *seq_lens,
+                              int B, int s, int max_seq_len, void *out, float *out_lse, void *workspace,
+                              size_t ws_bytes, uint32_t flags, void *stream)
+{
+    mla_status_t st = check_dims(dims);
+    if (st != MLA_OK) return st;
+    if (B < 0 || s <= 0 || num_blocks < 0 || max_blocks < 0 || max_seq_len < s) return MLA_ERR_INVALID_ARG;
+    if (B == 0) return MLA_OK;
+    if (num_blocks == 0 || max_blocks == 0) return MLA_ERR_INVALID_ARG;
+    if (!q_nope || !q_rope || !w_uk || !w_uv || !codes || !scales || !block_table || !seq_lens || !out)
+        return MLA_ERR_INVALID_ARG;
+    if (!aligned16(q_nope) || !aligned16(q_rope) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned16(codes) ||
+        !aligned16(scales) || !aligned16(out))
+        return MLA_ERR_INVALID_ARG;
+    // 127: run_prefill rounds max_seq_len up to a multiple of 128; 65535: the
+    // grid's limit on sequences
+    if (!int4_sizes_ok(B, s, dims->num_heads, max_blocks) || max_seq_len > (1ll << 31) - 1 - 127 || B > 65535)
+        return MLA_ERR_UNSUPPORTED;
+    if (!workspace) return MLA_ERR_WORKSPACE;
+    return run_prefill(dims, q_nope, q_rope, q_pos, w_uk, w_uv,
+                       Int4Rows{(const uint8_t *)codes, (const uint8_t *)scales}, num_blocks, block_table, max_blocks,
+                       seq_lens, B, s, max_seq_len, out, out_lse, workspace, ws_bytes, flags, as_stream(stream));
 }
 
 mla_status_t mla_fold_weights(const mla_dims_t *dims, int d_q, const void *w_uq, const void *w_uk, void *w_qk,

@@ -37,6 +37,7 @@
 #pragma once
 
 #include "dec_common.cuh"
+#include "k_simple.cuh"
 
 namespace mla {
 
@@ -383,9 +384,11 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
 // block table into rows [b * lpad, b * lpad + lpad) of a contiguous [576]-wide
 // buffer (rows at or past the sequence's length, and every row of an invalid
 // sequence, are zero), and the chunk's RoPE queries rotated to q_pos (copied
-// when q_pos is null).
+// when q_pos is null).  Rows: how the cache's rows are read as bf16 (Bf16Rows,
+// Int4Rows).
+template <class Rows>
 __global__ void __launch_bounds__(256)
-prefill_prepare_kernel(const bf16 *__restrict__ cache, int num_blocks, const int32_t *__restrict__ block_table,
+prefill_prepare_kernel(const Rows cache, int num_blocks, const int32_t *__restrict__ block_table,
                        int max_blocks, const int32_t *__restrict__ seq_lens, int B, int s, int H, int lpad,
                        int l_cap, bf16 *__restrict__ rows, const bf16 *__restrict__ q_rope,
                        const int32_t *__restrict__ q_pos, bf16 *__restrict__ q_rot, const RopeTable rope,
@@ -406,7 +409,7 @@ prefill_prepare_kernel(const bf16 *__restrict__ cache, int num_blocks, const int
         if (valid && j < L) {
             const int blk = block_table[(long long)b * max_blocks + j / kBlock];
             if (blk >= 0 && blk < num_blocks)
-                v = reinterpret_cast<const uint4 *>(cache + ((long long)blk * kBlock + j % kBlock) * kRow)[c];
+                v = cache.unit((long long)blk * kBlock + j % kBlock, c);
             else if (c == 0)
                 set_error(err, MLA_DEVERR_BLOCK_ID);
         }

@@ -361,6 +361,82 @@ mla_status_t mla_decode_fp8(const mla_dims_t *dims, const void *q_abs, const voi
                             uint32_t flags, void *stream);
 
 /*
+ * 4-bit latent cache [DeepSeek-V2 paper review, sections 4 and 9: the deployed
+ * model keeps its KV cache at about 6 bits per element; DeepSeek-V3 report
+ * summary: fine-grained scaling factors].  A token's row [c^KV (512) | k^R
+ * (64), rotated] is cut into 36 groups of 16 values.  Each group has one scale
+ * byte b, standing for s = (1 + (b & 7) / 8) 2^((b >> 3) - 15), and 16 codes
+ * u in 0..15 standing for (u - 8) s.  Every such value is a bf16 value exactly,
+ * and every bit pattern of a page is a finite row.
+ *   codes  [num_blocks][block_size][(d_c + d_rope) / 2] uint8; the eight
+ *          values v0..v7 of a little-endian 32-bit word are its nibbles
+ *          v0 v2 v4 v6 v1 v3 v5 v7 from the lowest up
+ *   scales [num_blocks][block_size][(d_c + d_rope) / 16] uint8
+ * Both 16-byte aligned.  324 bytes a token (1152 in bf16, 584 in FP8).
+ *
+ * mla_append_latent_int4 -- mla_append_latent into the 4-bit cache: forms the
+ * same bf16 row (copy or RMSNorm of c_kv, RoPE of k_rope at pos) and writes
+ * its codes and scales to the slot of (seq_idx[t], pos[t]): s is the
+ * group's amax * (1/7), both in fp32, rounded to nearest-even at three mantissa
+ * bits and clamped to the range above; u = 8 + x / s (fp32), rounded to nearest-even, u - 8
+ * clamped to [-7, 7].  A NaN is stored as 0, an infinity as the largest value
+ * of the largest scale.  Arguments as for mla_append_latent, with `codes` and
+ * `scales` in place of `cache` (num_blocks pages of each).  T is at most 2^26
+ * (MLA_ERR_UNSUPPORTED).  The tokens' slots must differ: of two tokens with
+ * one slot, which one's codes and scales stay there is not defined.
+ */
+mla_status_t mla_append_latent_int4(const mla_dims_t *dims, const void *c_kv, const void *k_rope,
+                                    int T, const int32_t *seq_idx, const int32_t *pos,
+                                    const int32_t *block_table, int num_seqs, int max_blocks,
+                                    void *codes, void *scales, int num_blocks,
+                                    const void *kv_norm_weight, float kv_norm_eps,
+                                    uint32_t *err_word, void *stream);
+
+/*
+ * mla_gather_latent_int4 -- rows of the 4-bit cache as bf16 (their values
+ * exactly): rows[t] = the row of (seq_idx[t], pos[t]).  With it a stored
+ * prefix is handed to a bf16 cache (as the c_kv of mla_append_latent, or
+ * scattered by the caller) or looked at.
+ *   seq_idx, pos [T] int32 (device), in any order, repeats allowed
+ *   rows         [T][d_c + d_rope] bf16 (output), 16-byte aligned
+ *   err_word     optional device uint32; bits MLA_DEVERR_* are OR-ed in for
+ *                places whose slot is invalid (their rows are zero)
+ * T = 0 is a no-op.
+ */
+mla_status_t mla_gather_latent_int4(const mla_dims_t *dims, const void *codes, const void *scales,
+                                    int num_blocks, const int32_t *seq_idx, const int32_t *pos,
+                                    int T, const int32_t *block_table, int num_seqs, int max_blocks,
+                                    void *rows, uint32_t *err_word, void *stream);
+
+/*
+ * mla_decode_int4 -- mla_decode over the 4-bit cache: the same attention on the
+ * rows the cache stands for (bf16 operands, fp32 accumulation).  Arguments, flags,
+ * workspace (mla_decode_workspace_size), outputs and errors as for mla_decode,
+ * with `codes` and `scales` in place of `cache`.  B * s * num_heads and
+ * max_blocks * block_size must be below 2^31 (MLA_ERR_UNSUPPORTED).
+ */
+mla_status_t mla_decode_int4(const mla_dims_t *dims, const void *q_abs, const void *codes,
+                             const void *scales, int num_blocks, const int32_t *block_table,
+                             int max_blocks, const int32_t *seq_lens, int B, int s,
+                             void *out_latent, float *out_lse, void *workspace, size_t ws_bytes,
+                             uint32_t flags, void *stream);
+
+/*
+ * mla_prefill_int4 -- mla_prefill over the 4-bit cache: the same attention on
+ * the rows the cache stands for (the chunk's own rows included: append them
+ * first).  Arguments, workspace
+ * (mla_prefill_workspace_size), outputs and errors as for mla_prefill, with
+ * `codes` and `scales` in place of `cache`; at most 65,535 sequences, and the
+ * size limits of mla_decode_int4 (MLA_ERR_UNSUPPORTED).
+ */
+mla_status_t mla_prefill_int4(const mla_dims_t *dims, const void *q_nope, const void *q_rope,
+                              const int32_t *q_pos, const void *w_uk, const void *w_uv,
+                              const void *codes, const void *scales, int num_blocks,
+                              const int32_t *block_table, int max_blocks, const int32_t *seq_lens,
+                              int B, int s, int max_seq_len, void *out, float *out_lse,
+                              void *workspace, size_t ws_bytes, uint32_t flags, void *stream);
+
+/*
  * Weight pre-absorption [DeepSeek-V2 paper review, section 2: at inference
  * W^UK can be absorbed into the query up-projection W^UQ and W^UV into the
  * output projection W^O; the query path compresses to c^Q = W^DQ h of width

@@ -48,6 +48,9 @@ tests/test_oracle_pins.py, none is "parity unpinned":
     it are unchanged, the ramp is continuous, the rotation preserves norms;
   * fold_qk, fold_ov: identity W^UQ (or W^O) returning (U^K)^T (or the U^V
     blocks) exactly, and brute-force dot products on tiny integer inputs;
+  * int4_values, int4_quantize_rows: every (code, scale byte) pair against the
+    format's formula in exact rational arithmetic, the scale and the codes
+    against a brute-force search of the nearest ones;
   * absorb_q_folded, up_out_folded: equal to the pinned two-step path
     (absorb_q of W^UQ c^Q; out_proj of up_v) on the same inputs.
 """
@@ -336,6 +339,38 @@ def decode_latent_fp8_rows(codes, scales, block_table, seq_lens, s, q_abs, rows=
     if rc != 0:
         raise ValueError("block table entry out of range")
     return out, lse
+
+
+# ----------------------------------------------------------- 4-bit cache
+def int4_values(codes, scales) -> np.ndarray:
+    """Rows [...][2 n] (float64) of the 4-bit cache's codes [...][n] uint8 and
+    scale bytes [...][n / 8] uint8: (u - 8) * (1 + (b & 7) / 8) * 2^((b >> 3) - 15),
+    the values v0..v7 of a 32-bit word in nibbles v0 v2 v4 v6 v1 v3 v5 v7."""
+    codes = np.ascontiguousarray(codes, dtype=np.uint8)
+    b = np.asarray(scales, dtype=np.int64)
+    n = codes.shape[-1]
+    nib = np.stack([codes & 15, codes >> 4], axis=-1).reshape(codes.shape[:-1] + (n // 4, 8))
+    u = nib[..., [0, 4, 1, 5, 2, 6, 3, 7]].reshape(codes.shape[:-1] + (n // 8, 16)).astype(np.float64)
+    s = (1.0 + (b & 7) / 8.0) * np.exp2((b >> 3) - 15.0)
+    return ((u - 8.0) * s[..., None]).reshape(codes.shape[:-1] + (2 * n,))
+
+
+def int4_quantize_rows(rows):
+    """Cache rows [N][D] (float32; D a multiple of 16) -> (codes uint8
+    [N][D / 2], scale bytes uint8 [N][D / 16]) of the 4-bit cache: the scale
+    nearest to amax * (1/7) (both fp32), ties to the even byte, the code nearest to
+    x / s (fp32), ties to even, within [-7, 7]; a NaN counts as 0."""
+    x = np.ascontiguousarray(rows, dtype=np.float32)
+    x = np.where(np.isnan(x), np.float32(0), x).reshape(x.shape[0], -1, 16)
+    t = (np.abs(x).max(-1) * (np.float32(1) / np.float32(7))).astype(np.float64)
+    every = np.array([(1 + b % 8 / 8) * 2.0 ** (b // 8 - 15) for b in range(256)])
+    hi = np.clip(np.searchsorted(every, t), 1, 255)
+    up, down = every[hi] - t, t - every[hi - 1]
+    b = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, hi - 1)
+    s = every[b].astype(np.float32)[..., None]
+    u = (np.clip(np.rint(x / s), -7, 7) + 8).astype(np.uint8).reshape(x.shape[0], -1, 8)
+    nib = u[..., [0, 2, 4, 6, 1, 3, 5, 7]]
+    return (nib[..., 0::2] | nib[..., 1::2] << 4).reshape(x.shape[0], -1), b.astype(np.uint8)
 
 
 # ------------------------------------------------------------ append extras
