@@ -232,6 +232,18 @@ def test_decode_of_full_sized_batches(M):
             assert np.all(np.abs(lse[b:b + 1, ::5] - rlse) <= tol_lse)
 
 
+def test_stall_hook_reports_a_timeout(M):
+    cfg = C("stall", 128, [700, 129], seed=24)
+    d = W.make_decode_inputs(cfg, with_cache_pages=False)
+    codes, scales = random_cache(d, 24)
+    q = W.make_q_abs(cfg)
+    good, _, _ = run_decode(M, cfg, d, codes, scales, q)
+    _, _, err = run_decode(M, cfg, d, codes, scales, q, M.MLA_DEBUG_STALL)
+    assert err & M.MLA_DEVERR_TIMEOUT
+    again, _, err = run_decode(M, cfg, d, codes, scales, q)
+    assert err == 0 and np.array_equal(again, good)
+
+
 # ------------------------------------------------------------ writer, reader
 def append(M, dims, rows_c, rows_k, seq, pos, table, nb, fill=0xFF, **kw):
     import torch
