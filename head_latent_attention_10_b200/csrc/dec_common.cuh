@@ -31,7 +31,6 @@ struct DecArgs {
     int stall_tile;       // test hook: the page load of this tile of every range is never issued (-1: none)
     int merges;           // merge two-piece sequences in the decode kernel (0: the combine merges all)
     const float *scales;  // FP8 cache only: [num_blocks][64][2] fp32 per-part scales
-    const uint8_t *codes4, *scales4;   // 4-bit cache only: [num_blocks][64][288], [num_blocks][64][36]
     float scale_log2;
     int max_blocks, num_blocks, s, H, B, groups;
 };

@@ -15,6 +15,7 @@
 #include "int4.cuh"
 #include "k_simple.cuh"
 #include "tc_decode64.cuh"
+#include "tc_decode_int4.cuh"
 #include "tc_gemm.cuh"
 #include "tc_prefill.cuh"
 #include "tmap.cuh"
@@ -264,7 +265,7 @@ int decode_ranges(int H, int s)
     static std::atomic<bool> attr64[kMaxDevices];
     const int sms = sm_count();
     if (sms <= 0) return 0;
-    if (ensure_smem_attr(tc_decode64_kernel<kBf16>, kD64Smem, attr64) != cudaSuccess) return 0;
+    if (ensure_smem_attr(tc_decode64_kernel<false>, kD64Smem, attr64) != cudaSuccess) return 0;
     const int groups = dec_groups(H, s);
     int r = sms / groups;
     const int cap = kMaxRanges / groups;
@@ -272,10 +273,10 @@ int decode_ranges(int H, int s)
     return r > 0 ? r : 1;
 }
 
-// The tensor-core decode (plan, decode kernel, combine) on a bf16 cache, an FP8
-// cache (codes + per-part scales) or a 4-bit cache (codes + group scales).
-template <int kCache>
-mla_status_t run_tc_decode(const mla_dims_t *dims, const void *q_abs, const void *cache, const void *scales,
+// The tensor-core decode (plan, decode kernel, combine) on a bf16 cache, or
+// on an FP8 cache (codes + per-part scales) with kFp8.
+template <bool kFp8>
+mla_status_t run_tc_decode(const mla_dims_t *dims, const void *q_abs, const void *cache, const float *scales,
                            int num_blocks, const int32_t *block_table, int max_blocks, const int32_t *seq_lens,
                            int B, int s, void *out_latent, float *out_lse, char *ws, size_t ws_bytes,
                            uint32_t flags, cudaStream_t strm)
@@ -287,16 +288,13 @@ mla_status_t run_tc_decode(const mla_dims_t *dims, const void *q_abs, const void
     const int groups = dec_groups(H, s);
     const int ranges = decode_ranges(H, s);
     if (ranges <= 0) return MLA_ERR_CUDA;
-    CUtensorMap mkv = {};
-    if (kCache == kInt4) {   // read by plain loads: no tensor map
-        static std::atomic<bool> attr4[kMaxDevices];
-        if (ensure_smem_attr(tc_decode64_kernel<kInt4>, kD64Smem, attr4) != cudaSuccess) return MLA_ERR_CUDA;
-    } else if (kCache == kFp8Cache) {
+    CUtensorMap mkv;
+    if (kFp8) {
         if (!make_tmap_3d_u8(&mkv, cache, kRow, (uint64_t)num_blocks * kBlock, 1, kRow, (uint64_t)num_blocks * kBlock * kRow,
                              64, kT64, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
             return MLA_ERR_CUDA;
         static std::atomic<bool> attr8[kMaxDevices];
-        if (ensure_smem_attr(tc_decode64_kernel<kFp8Cache>, kD64SmemFp8, attr8) != cudaSuccess) return MLA_ERR_CUDA;
+        if (ensure_smem_attr(tc_decode64_kernel<true>, kD64SmemFp8, attr8) != cudaSuccess) return MLA_ERR_CUDA;
     } else {
         if (!tmap(&mkv, cache, kRow, (uint64_t)num_blocks * kBlock, 1, kRow, 0, 64, kT64)) return MLA_ERR_CUDA;
     }
@@ -317,9 +315,7 @@ mla_status_t run_tc_decode(const mla_dims_t *dims, const void *q_abs, const void
     da.limit_ns = (flags & MLA_DEBUG_STALL) ? kStallWaitLimitNs : kWaitLimitNs;
     da.stall_tile = (flags & MLA_DEBUG_STALL) ? 0 : -1;
     da.merges = (flags & MLA_DEBUG_COMBINE_ALL) ? 0 : 1;
-    da.scales = kCache == kFp8Cache ? (const float *)scales : nullptr;
-    da.codes4 = kCache == kInt4 ? (const uint8_t *)cache : nullptr;
-    da.scales4 = kCache == kInt4 ? (const uint8_t *)scales : nullptr;
+    da.scales = scales;
     da.scale_log2 = softmax_scale(dims) * kLog2e;
     da.max_blocks = max_blocks;
     da.num_blocks = num_blocks;
@@ -329,8 +325,9 @@ mla_status_t run_tc_decode(const mla_dims_t *dims, const void *q_abs, const void
     da.groups = groups;
     // the decode kernel sets itself up while the kernel before it ends, and
     // the combine launches while the decode's last CTAs finish
-    cudaError_t e = launch_pdl(tc_decode64_kernel<kCache>, dim3(ranges * groups), dim3(d64_threads(kCache)),
-                               kCache == kFp8Cache ? kD64SmemFp8 : kD64Smem, strm, mkv, da);
+    cudaError_t e = launch_pdl(tc_decode64_kernel<kFp8>, dim3(ranges * groups),
+                               dim3(kFp8 ? kD64ThreadsFp8 : kD64Threads), kFp8 ? kD64SmemFp8 : kD64Smem, strm, mkv,
+                               da);
     count_launch();
     if (e != cudaSuccess) return MLA_ERR_CUDA;
     static std::atomic<bool> attr_cb[kMaxDevices];
@@ -340,6 +337,67 @@ mla_status_t run_tc_decode(const mla_dims_t *dims, const void *q_abs, const void
     e = launch_pdl(dec_combine_kernel, dim3(cgrid), dim3(kCombineThreads), kCombineSmem, strm, (const int32_t *)plan,
                    (const int *)da.flags, (const float *)da.part_o, (const float *)da.part_lse2, B, s, H,
                    (bf16 *)out_latent, out_lse, err, da.limit_ns);
+    count_launch();
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+// Ranges (persistent CTAs per row group) of the 4-bit decode on the current
+// device: one CTA per SM.
+int decode_int4_ranges(int groups)
+{
+    const int sms = sm_count();
+    if (sms <= 0) return 0;
+    const int r = (sms < kMaxRanges ? sms : kMaxRanges) / groups;
+    return r > 0 ? r : 1;
+}
+
+// The tensor-core decode (plan, decode kernel, combine) on the 4-bit cache.
+mla_status_t run_int4_decode(const mla_dims_t *dims, const void *q_abs, const void *codes, const void *scales,
+                             int num_blocks, const int32_t *block_table, int max_blocks, const int32_t *seq_lens,
+                             int B, int s, void *out_latent, float *out_lse, char *ws, size_t ws_bytes,
+                             uint32_t flags, cudaStream_t strm)
+{
+    const int H = dims->num_heads;
+    const TcWs w = tc_ws(H, s, B);
+    if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
+    static std::atomic<bool> attr4[kMaxDevices], attr_cb[kMaxDevices];
+    if (ensure_smem_attr(tc_decode_int4_kernel, kD4Smem, attr4) != cudaSuccess ||
+        ensure_smem_attr(dec_combine_kernel, kCombineSmem, attr_cb) != cudaSuccess)
+        return MLA_ERR_CUDA;
+    const int groups = dec_groups(H, s), ranges = decode_int4_ranges(groups);
+    if (ranges <= 0) return MLA_ERR_CUDA;
+    // the error word, the plan and the combine's flags
+    if (cudaMemsetAsync(ws, 0, w.off_zero_end, strm) != cudaSuccess) return MLA_ERR_CUDA;
+    int *cflags = (int *)(ws + w.off_flags);
+    Dec4Args da;
+    da.q_abs = (const bf16 *)q_abs;
+    da.codes = (const uint8_t *)codes;
+    da.scales = (const uint8_t *)scales;
+    da.block_table = block_table;
+    da.seq_lens = seq_lens;
+    da.plan = (int32_t *)(ws + w.off_plan);
+    da.work = cflags + 2 * (size_t)B * groups * 4;
+    da.out = (bf16 *)out_latent;
+    da.out_lse = out_lse;
+    da.part_o = (float *)(ws + w.off_o);
+    da.part_lse2 = (float *)(ws + w.off_lse);
+    da.err = (uint32_t *)ws;
+    da.limit_ns = (flags & MLA_DEBUG_STALL) ? kStallWaitLimitNs : kWaitLimitNs;
+    da.stall_tile = (flags & MLA_DEBUG_STALL) ? 0 : -1;
+    da.scale_log2 = softmax_scale(dims) * kLog2e;
+    da.max_blocks = max_blocks;
+    da.num_blocks = num_blocks;
+    da.s = s;
+    da.H = H;
+    da.B = B;
+    da.groups = groups;
+    cudaError_t e = launch_pdl(tc_decode_int4_kernel, dim3(ranges * groups), dim3(kD4Threads), kD4Smem, strm, da);
+    count_launch();
+    if (e != cudaSuccess) return MLA_ERR_CUDA;
+    const int blocks = combine_blocks(B, s, H), most = kCombineCtasPerSm * sm_count();
+    e = launch_pdl(dec_combine_kernel, dim3(blocks < most ? blocks : most), dim3(kCombineThreads), kCombineSmem, strm,
+                   (const int32_t *)da.plan, (const int *)cflags, (const float *)da.part_o, (const float *)da.part_lse2,
+                   B, s, H, (bf16 *)out_latent, out_lse, da.err, da.limit_ns);
     count_launch();
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
@@ -654,7 +712,7 @@ mla_status_t mla_decode(const mla_dims_t *dims, const void *q_abs, const void *c
                                                  max_blocks, seq_lens, B, s, out_latent, out_lse, ws, ws_bytes, strm);
         if (r != MLA_OK) return r;
     } else {
-        const mla_status_t r = run_tc_decode<kBf16>(dims, q_abs, cache, nullptr, num_blocks, block_table, max_blocks,
+        const mla_status_t r = run_tc_decode<false>(dims, q_abs, cache, nullptr, num_blocks, block_table, max_blocks,
                                                     seq_lens, B, s, out_latent, out_lse, ws, ws_bytes, flags, strm);
         if (r != MLA_OK) return r;
     }
@@ -801,7 +859,7 @@ mla_status_t mla_decode_fp8(const mla_dims_t *dims, const void *q_abs, const voi
     if (!workspace) return MLA_ERR_WORKSPACE;
     cudaStream_t strm = as_stream(stream);
     char *ws = (char *)workspace;
-    const mla_status_t r = run_tc_decode<kFp8Cache>(dims, q_abs, codes, scales, num_blocks, block_table, max_blocks,
+    const mla_status_t r = run_tc_decode<true>(dims, q_abs, codes, scales, num_blocks, block_table, max_blocks,
                                                seq_lens, B, s, out_latent, out_lse, ws, ws_bytes, flags, strm);
     if (r != MLA_OK) return r;
     if (flags & MLA_SYNC_CHECK) {
@@ -878,8 +936,8 @@ mla_status_t mla_decode_int4(const mla_dims_t *dims, const void *q_abs, const vo
         (flags & MLA_FORCE_SIMPLE)
             ? run_simple_decode(dims, q_abs, Int4Rows{(const uint8_t *)codes, (const uint8_t *)scales}, num_blocks,
                                 block_table, max_blocks, seq_lens, B, s, out_latent, out_lse, ws, ws_bytes, strm)
-            : run_tc_decode<kInt4>(dims, q_abs, codes, scales, num_blocks, block_table, max_blocks, seq_lens, B, s,
-                                   out_latent, out_lse, ws, ws_bytes, flags, strm);
+            : run_int4_decode(dims, q_abs, codes, scales, num_blocks, block_table, max_blocks, seq_lens, B, s,
+                              out_latent, out_lse, ws, ws_bytes, flags, strm);
     if (r != MLA_OK) return r;
     if (flags & MLA_SYNC_CHECK) {
         uint32_t host = 0;

@@ -79,24 +79,10 @@
 // 8,192 j, so output chunk j overwrites the codes of chunks 2j-9 and 2j-8: the
 // converters go in four groups (0-3 | 4-5 | 6 | 7-8) with a named barrier
 // between groups, and chunk 8's codes are read before the last barrier.
-//
-// 4-bit cache (kInt4): a page is 288 B of codes and 36 scale bytes per token
-// (csrc/int4.cuh), and every value is a bf16 value, so the MMAs, Q, P and the
-// softmax are the bf16 path's and only the way a page reaches its stage
-// differs.  Eight converter warps (8-15) read codes and scales from global
-// memory into registers one tile ahead, and when the stage is free widen them
-// straight into the tile layout: no codes in shared memory (the three stages
-// fill it), no copy to wait for in the stage's life, and no hazard between a
-// page's codes and its values.  Thread ct takes 16 values (one scale) of each
-// 64-column chunk of row ct / 4.  Warp 0 only warms L2.  Every pattern a page
-// can hold is finite, so rows past a sequence's end need no zeroing.  The
-// warps' registers are split by role (kD64Regs..): the softmax warps hold a
-// row of queries at a switch.
 #pragma once
 
 #include "dec_common.cuh"
 #include "fp8.cuh"
-#include "int4.cuh"
 
 namespace mla {
 
@@ -117,7 +103,6 @@ constexpr uint32_t kD64TmO = 16u << 16;           // O: lanes 16-31, columns 0-5
 constexpr uint32_t kD64TmQ = 128;                 // Q: lanes 0-15, columns 128-415 (S: 0-127)
 constexpr uint32_t kD64TmS2 = 416;                // third logits buffer: lanes 0-15, columns 416-479
 constexpr int kD64Ahead = 1;                      // tiles prefetched into L2 ahead of the load
-constexpr int kD64AheadInt4 = 3;                  // the same for the 4-bit cache, ahead of the tile being widened
 // FP8 cache: 128 more threads (the converters), per-stage scale slots
 // ([64][2] fp32) and per-token factored scales s_j ([64] fp32) after the stages
 constexpr int kD64Cvt = 128;                       // converter threads (warps 8-11)
@@ -131,33 +116,15 @@ constexpr int kD64OffBarFp8 = kD64OffSmax + kD64Stages * 256;
 constexpr int kD64OffEpiFp8 = kD64OffBarFp8 + 512;
 constexpr int kD64SmemFp8 = kD64OffEpiFp8 + 4 * 16 * kD64EpiRowFp8 + 1024;
 
-// 4-bit cache: eight converter warps
-constexpr int kD64CvtInt4 = 256;
-constexpr int kD64ThreadsInt4 = kD64Threads + kD64CvtInt4;   // 512: 128 registers a thread at launch
-// registers a thread per warpgroup (warps 0-3, the softmax warps, the converters):
-// 128 (104 + 200 + 2 * 104) = 65,536, what the CTA is launched with
-constexpr int kD64RegsIssue = 104, kD64RegsSoftmax = 200, kD64RegsCvt = 104;
-
-enum : int { kBf16 = 0, kFp8Cache = 1, kInt4 = 2 };   // the cache a decode kernel reads
-
-__host__ __device__ constexpr int d64_threads(int cache)
-{
-    return cache == kInt4 ? kD64ThreadsInt4 : cache == kFp8Cache ? kD64ThreadsFp8 : kD64Threads;
-}
-
-template <int kCache>
-__global__ void __launch_bounds__(d64_threads(kCache), 1)
+template <bool kFp8>
+__global__ void __launch_bounds__(kFp8 ? kD64ThreadsFp8 : kD64Threads, 1)
 tc_decode64_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a)
 {
-    constexpr bool kFp8 = kCache == kFp8Cache;
-    constexpr bool kWiden = kCache != kBf16;       // the stages are filled by converter warps
-    constexpr bool kMerge = kCache != kFp8Cache;   // two-piece merges in this kernel
     extern __shared__ uint8_t d64_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(d64_smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + (kFp8 ? kD64OffBarFp8 : kD64OffBar));
-    uint64_t *cv_full = bars + 32;   // [3] FP8, 4-bit: the stage's codes widened (the converter warps)
-    volatile int *cvt_at = reinterpret_cast<volatile int *>(bars + 38);   // 4-bit: the tile being widened
+    uint64_t *cv_full = bars + 32;   // [3] FP8: the stage's codes widened to f16 (the converter warps)
     uint64_t *kv_full = bars + 18;   // [3] TMA -> MMA (bf16: chunks 5-8 of the page)
     uint64_t *kv_half = bars + 35;   // [3] bf16: chunks 0-4 of the page landed
     uint64_t *kv_empty = bars + 21;  // [3] P.C MMAs of the stage done -> TMA, softmax
@@ -186,20 +153,18 @@ tc_decode64_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a)
             sm100::mbar_init(&kv_half[i], 1);
         }
         *q_cnt = 0;
-        *cvt_at = 0;
         for (int i = 0; i < 3; ++i) {
             sm100::mbar_init(&s_full[i], 1);
             sm100::mbar_init(&s_free[i], 4);
         }
         for (int i = 0; i < kD64Stages; ++i) p_cnt[i] = 0;
-        if constexpr (kWiden)
-            for (int i = 0; i < kD64Stages; ++i)
-                sm100::mbar_init(&cv_full[i], (kCache == kInt4 ? kD64CvtInt4 : kD64Cvt) / 32);
+        if constexpr (kFp8)
+            for (int i = 0; i < kD64Stages; ++i) sm100::mbar_init(&cv_full[i], kD64Cvt / 32);
         sm100::mbar_init(mma_done, 7);
         for (int i = 0; i < 4; ++i) sm100::mbar_init(&early_in[i], 1);
         *abort_flag = 0;
         sm100::fence_mbar_init();
-        if constexpr (kCache != kInt4) sm100::prefetch_tensormap(&map_kv);
+        sm100::prefetch_tensormap(&map_kv);
     }
     if (warp == 1) {
         sm100::tmem_alloc(tmem_slot, 512);
@@ -209,7 +174,7 @@ tc_decode64_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a)
     sm100::pdl_wait();
     if (warp == 2)
         plan_range(a.seq_lens, a.B, a.s, a.max_blocks, gridDim.x / a.groups, rng, blockIdx.x == 0,
-                   kMerge && a.merges, a.plan, a.flags + 2 * a.B * a.groups * 4, a.err, rplan);
+                   !kFp8 && a.merges, a.plan, a.flags + 2 * a.B * a.groups * 4, a.err, rplan);
     sm100::tc_fence_before();
     __syncthreads();
     sm100::tc_fence_after();
@@ -230,40 +195,7 @@ tc_decode64_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a)
         return (blk < 0 || blk >= a.num_blocks) ? -1 : blk;
     };
 
-    if constexpr (kCache == kInt4) {
-        // every warp of a warpgroup takes its share; the CTA's launch covers the sum
-        if (warp < 4)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kD64RegsIssue));
-        else if (warp < 8)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kD64RegsSoftmax));
-        else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kD64RegsCvt));
-    }
-    if (kCache == kInt4 && warp == 0) {
-        // ------------------------------------------------- L2 prefetch (4-bit)
-        // the page kD64AheadInt4 tiles beyond the one the converters are at, and the
-        // queries of a segment that starts there.  Nothing waits for this warp,
-        // so it follows a count, not a barrier's phase, which could lap it
-        TileIter it;
-        it.init(a.seq_lens, a.max_blocks, a.B, lo, hi, seq0, start0, va0);
-        for (; it.ok; it.advance()) {
-            if (!wait_count(cvt_at, it.k - kD64AheadInt4, abort_flag, a.err, lim)) break;
-            if (lane == 0 && it.k > 0) {
-                if (it.first()) {
-                    const int r0 = group * kGroupRows, nr = min(kGroupRows, rows_per_seq - r0);
-                    const char *q0 = reinterpret_cast<const char *>(a.q_abs + ((long long)it.seq * rows_per_seq + r0) * kRow);
-                    for (int r = 0; r < nr; r += 8)
-                        sm100::bulk_prefetch_l2(q0 + (long long)r * kRow * 2, min(8, nr - r) * kRow * 2);
-                }
-                const int pb = page_of(it);
-                if (pb >= 0) {
-                    sm100::bulk_prefetch_l2(a.codes4 + (long long)pb * (kBlock * kInt4Codes), kBlock * kInt4Codes);
-                    sm100::bulk_prefetch_l2(a.scales4 + (long long)pb * (kBlock * kInt4Scales), kBlock * kInt4Scales);
-                }
-            }
-            __syncwarp();
-        }
-    } else if (warp == 0) {
+    if (warp == 0) {
         // ------------------------------------------------------------ TMA
         if (lane == 0) {
             TileIter it, ahead;
@@ -367,7 +299,7 @@ tc_decode64_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a)
                 q_seg = is.seg;
             }
             if (!ok) break;
-            ok = sm100::warp_wait(kWiden ? &cv_full[st] : &kv_half[st], (kk / kD64Stages) & 1, abort_flag, a.err, lim);
+            ok = sm100::warp_wait(kFp8 ? &cv_full[st] : &kv_half[st], (kk / kD64Stages) & 1, abort_flag, a.err, lim);
             if (ok && kk >= 3) ok = sm100::warp_wait(&s_free[b], ((kk / 3) - 1) & 1, abort_flag, a.err, lim);
             if (!ok) break;
             sm100::tc_fence_after();
@@ -377,7 +309,7 @@ tc_decode64_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a)
                 const uint32_t d = tmem + scol;
 #pragma unroll
                 for (int step = 0; step < 36; ++step) {          // 16-column K steps
-                    if (!kWiden && step == 20) {
+                    if (!kFp8 && step == 20) {
                         // chunks 5-8 (the bf16 page's second half)
                         if (!sm100::mbar_wait(&kv_full[st], (kk / kD64Stages) & 1, abort_flag, a.err, lim)) {
                             ok2 = 0;
@@ -393,72 +325,6 @@ tc_decode64_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a)
             ok = __shfl_sync(0xffffffffu, ok2, 0) != 0;
             __syncwarp();
             is.advance();
-        }
-    } else if (kCache == kInt4 && warp >= 8) {
-        // ------------------------------------------- 4-bit -> bf16 (warps 8-15)
-        const int ct = threadIdx.x - kD64Threads, r = ct >> 2, g = ct & 3;
-        const int ntile = hi - lo;
-        TileIter it;   // two tiles ahead of the one being widened
-        it.init(a.seq_lens, a.max_blocks, a.B, lo, hi, seq0, start0, va0);
-        // the page of the next tile in the list; a bad entry reads page 0 and is reported
-        auto next_page = [&]() -> int {
-            if (!it.ok) return 0;
-            int blk = page_of(it);
-            if (blk < 0) {
-                if (ct == 0) set_error(a.err, MLA_DEVERR_BLOCK_ID);
-                blk = 0;
-            }
-            it.advance();
-            return blk;
-        };
-        // a page's 9 code pairs and the row's scale words as this thread holds them:
-        // words g, g + 4 and 8 of the row's nine (word j: the four scales of
-        // chunk j), the quad's other words through shuffles.  The page may have
-        // been written by the kernel before this one: through L2.
-        struct Page {
-            uint2 c[9];
-            uint32_t s0, s1, s8;
-        };
-        auto load = [&](Page &p, int blk) {
-            const uint2 *src = reinterpret_cast<const uint2 *>(a.codes4 + ((long long)blk * kBlock + r) * kInt4Codes) + g;
-            const uint32_t *sc = reinterpret_cast<const uint32_t *>(a.scales4 + ((long long)blk * kBlock + r) * kInt4Scales);
-#pragma unroll
-            for (int j = 0; j < 9; ++j) p.c[j] = __ldcg(src + 4 * j);
-            p.s0 = __ldcg(sc + g);
-            p.s1 = __ldcg(sc + 4 + g);
-            p.s8 = __ldcg(sc + 8);
-        };
-        Page cur, nxt;
-        load(cur, next_page());
-        int blk1 = next_page();
-        bool ok = true;
-        const uint32_t row = sm100::smem_u32(stages) + r * 128, sw = r & 7;
-        for (int k = 0; k < ntile; ++k) {
-            const int st = k % kD64Stages;
-            const int blk2 = next_page();   // in flight during this tile
-            if (k + 1 < ntile) load(nxt, blk1);
-            blk1 = blk2;
-            if (ct == 0) *cvt_at = k;
-            if (k >= kD64Stages)
-                ok = sm100::warp_wait(&kv_empty[st], ((k / kD64Stages) - 1) & 1, abort_flag, a.err, lim);
-            if (!ok) break;
-            if (k != a.stall_tile) {   // test hook: this tile never becomes full
-                const uint32_t base = row + st * kD64Stage;
-#pragma unroll
-                for (int j = 0; j < 9; ++j) {
-                    uint32_t sw4 = cur.s8;   // chunk j's four scales
-                    if (j < 8) sw4 = __shfl_sync(0xffffffffu, j < 4 ? cur.s0 : cur.s1, j & 3, 4);
-                    __nv_bfloat162 s2, m24s2;
-                    int4_scale2(__byte_perm(sw4, 0, 0x4440 + g), s2, m24s2);
-                    const uint32_t dst = base + j * kD64Chunk;
-                    st_shared_v4(dst + (((2 * g) ^ sw) << 4), int4_widen8(cur.c[j].x, s2, m24s2));
-                    st_shared_v4(dst + (((2 * g + 1) ^ sw) << 4), int4_widen8(cur.c[j].y, s2, m24s2));
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) sm100::mbar_arrive(&cv_full[st]);
-            }
-            cur = nxt;
         }
     } else if (kFp8 && warp >= 8) {
         // ----------------------------------------------- FP8 -> f16 (warps 8-11)
@@ -618,7 +484,7 @@ tc_decode64_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a)
                 // this warp's quarter into L2 before the merge reads them
                 const int cf = (it.seq_v + kSwitchTiles) / qv, cl = (it.seq_v + kSwitchTiles + it.seq_t - 1) / qv;
                 const int r0 = group * kGroupRows + 16 * qd;
-                if (kMerge && a.merges && !it.complete && cl == cf + 1 && rng == cf && r0 < rows_per_seq) {
+                if (!kFp8 && a.merges && !it.complete && cl == cf + 1 && rng == cf && r0 < rows_per_seq) {
                     const char *e = reinterpret_cast<const char *>(a.part_o + (2LL * cl * rows_per_seq + r0) * kDc);
                     const int nr = min(16, rows_per_seq - r0);
                     for (int o = 0; o < nr * kDc * 4; o += 16384)
@@ -719,7 +585,7 @@ tc_decode64_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a)
                     st_shared_v4(p_row0 + (k % kD64Stages) * kD64Stage + (((c0 + c) ^ (r & 7)) << 4),
                                  make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]));
             }
-            if constexpr (kCache != kInt4) {
+            {
                 // a ragged last tile: zero the latent rows past the sequence end so
                 // that 0 * (whatever the page holds there) stays 0 (warp q: chunks 2q, 2q+1)
                 const int valid = min(kT64, nseq - it.tt * kT64);
@@ -865,7 +731,7 @@ tc_decode64_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a)
                 int *qflag = a.flags + (it.seq * a.groups + group) * 4 + qd;   // early; merged at + B groups 4
                 const int nq = a.B * a.groups * 4;
                 bool merge = false;
-                if (kMerge && two && rng == c_first) {   // (the FP8 kernel leaves every merge to the combine)
+                if (!kFp8 && two && rng == c_first) {   // (the FP8 kernel leaves every merge to the combine)
                     int rd = 0;
                     if (lane == 0) rd = ld_acquire_gpu(qflag);
                     merge = __shfl_sync(0xffffffffu, rd, 0) != 0;
@@ -945,9 +811,9 @@ tc_decode64_kernel(const __grid_constant__ CUtensorMap map_kv, const DecArgs a)
                             a.part_lse2[slot * rows_per_seq + grow_row] = lse2;
                         }
                     }
-                    if (kMerge && two && rng == c_first && lane == 0)
+                    if (!kFp8 && two && rng == c_first && lane == 0)
                         atomicAdd(a.flags + 2 * nq, 1);   // this quarter falls back to the combine
-                    if (kMerge && two && rng == c_last) {
+                    if (!kFp8 && two && rng == c_last) {
                         // the early piece's rows of this quarter are written
                         __threadfence();
                         __syncwarp();
