@@ -286,23 +286,23 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
         auto words_of = [&](int page) {
             return reinterpret_cast<const uint32_t *>(a.scales + ((long long)page * kBlock + r) * kInt4Scales);
         };
-        auto piece = [&](const uint8_t *src, int c) {
-            const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(src + 64 * c) + p);
-            return up ? make_uint4(v.z, v.w, v.x, v.y) : v;
-        };
+        auto piece = [&](const uint8_t *src, int c) { return __ldcg(reinterpret_cast<const uint4 *>(src + 64 * c) + p); };
         // what this thread holds of the page it will widen next: its pieces, its
         // part of chunk 8, and scale words p, p + 4 and 8 of the row's nine (word
-        // j: the four scales of chunk j)
+        // j: the four scales of chunk j).  The loop below reloads each register in
+        // place and touches it only a page later: a copy or a select on it there
+        // would wait for the load
         Dec4Tile t;
         bool ok = tile_at(0, t);
-        uint4 q0, q1, q2, q3;
+        uint4 q[4];
         uint2 c8;
         uint32_t s0, s1, s8;
         if (ok) {
             const uint8_t *src = src_of(t.page);
             const uint32_t *sc = words_of(t.page);
             s0 = __ldcg(sc + p); s1 = __ldcg(sc + 4 + p); s8 = __ldcg(sc + 8);
-            q0 = piece(src, 0); q1 = piece(src, 1); q2 = piece(src, 2); q3 = piece(src, 3);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) q[c] = piece(src, c);
             c8 = __ldcg(reinterpret_cast<const uint2 *>(src + 256) + p);
         }
         for (int k = 0; ok && k < ntile; ++k) {
@@ -320,26 +320,26 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
             if (!ok) break;
             if (k == a.stall_tile) continue;   // test hook: this tile never becomes full
             uint32_t dst = row + st * kD4Stage;
-#pragma unroll 1
+#pragma unroll
             for (int c = 0; c < 4; ++c) {
                 // the pair's scale word: word 2 c + (p >> 1) of the row
                 const uint32_t w = __shfl_sync(0xffffffffu, c < 2 ? s0 : s1, ((2 * c) & 3) + (p >> 1), 4);
                 __nv_bfloat162 a2, am, b2, bm;
                 int4_scale2(__byte_perm(w, 0, sel0), a2, am);
                 int4_scale2(__byte_perm(w, 0, sel1), b2, bm);
-                // words x, y share a scale, z, w the other; the upper chunk's
-                // pieces were read in the order z, w, x, y
+                // words x, y take the first scale, z, w the second; the upper
+                // chunk's pieces store z, w first
+                const uint4 v = up ? make_uint4(q[c].z, q[c].w, q[c].x, q[c].y) : q[c];
+                if (more) q[c] = piece(src, c);
                 if (up) {
                     const __nv_bfloat162 t2 = a2, tm = am;
                     a2 = b2; am = bm; b2 = t2; bm = tm;
                 }
-                st_shared_v4(dst + o0, int4_widen8(q0.x, a2, am));
-                st_shared_v4(dst + o1, int4_widen8(q0.y, a2, am));
-                st_shared_v4(dst + o2, int4_widen8(q0.z, b2, bm));
-                st_shared_v4(dst + o3, int4_widen8(q0.w, b2, bm));
+                st_shared_v4(dst + o0, int4_widen8(v.x, a2, am));
+                st_shared_v4(dst + o1, int4_widen8(v.y, a2, am));
+                st_shared_v4(dst + o2, int4_widen8(v.z, b2, bm));
+                st_shared_v4(dst + o3, int4_widen8(v.w, b2, bm));
                 dst += 2 * kD4Chunk;
-                q0 = q1; q1 = q2; q2 = q3;
-                if (more) q3 = piece(src, c);
             }
             {
                 __nv_bfloat162 a2, am;
