@@ -342,12 +342,15 @@ mla_status_t run_tc_decode(const mla_dims_t *dims, const void *q_abs, const void
 }
 
 // Ranges (persistent CTAs per row group) of the 4-bit decode on the current
-// device: one CTA per SM.
-int decode_int4_ranges(int groups)
+// device: one CTA per SM, fewer where the table holds so few pages that a
+// range would get less than kD4MinTiles of them.
+int decode_int4_ranges(int groups, int B, int max_blocks)
 {
     const int sms = sm_count();
     if (sms <= 0) return 0;
-    const int r = (sms < kMaxRanges ? sms : kMaxRanges) / groups;
+    int r = (sms < kMaxRanges ? sms : kMaxRanges) / groups;
+    const long long most = ((long long)B * max_blocks + kD4MinTiles - 1) / kD4MinTiles;
+    if (r > most) r = (int)most;
     return r > 0 ? r : 1;
 }
 
@@ -360,13 +363,11 @@ mla_status_t run_int4_decode(const mla_dims_t *dims, const void *q_abs, const vo
     const int H = dims->num_heads;
     const TcWs w = tc_ws(H, s, B);
     if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
-    static std::atomic<bool> attr4[kMaxDevices], attr_cb[kMaxDevices];
-    if (ensure_smem_attr(tc_decode_int4_kernel, kD4Smem, attr4) != cudaSuccess ||
-        ensure_smem_attr(dec_combine_kernel, kCombineSmem, attr_cb) != cudaSuccess)
-        return MLA_ERR_CUDA;
-    const int groups = dec_groups(H, s), ranges = decode_int4_ranges(groups);
+    static std::atomic<bool> attr4[kMaxDevices];
+    if (ensure_smem_attr(tc_decode_int4_kernel, kD4Smem, attr4) != cudaSuccess) return MLA_ERR_CUDA;
+    const int groups = dec_groups(H, s), ranges = decode_int4_ranges(groups, B, max_blocks);
     if (ranges <= 0) return MLA_ERR_CUDA;
-    // the error word, the plan and the combine's flags
+    // the error word, the plan and its count
     if (cudaMemsetAsync(ws, 0, w.off_zero_end, strm) != cudaSuccess) return MLA_ERR_CUDA;
     int *cflags = (int *)(ws + w.off_flags);
     Dec4Args da;
@@ -394,10 +395,13 @@ mla_status_t run_int4_decode(const mla_dims_t *dims, const void *q_abs, const vo
     cudaError_t e = launch_pdl(tc_decode_int4_kernel, dim3(ranges * groups), dim3(kD4Threads), kD4Smem, strm, da);
     count_launch();
     if (e != cudaSuccess) return MLA_ERR_CUDA;
-    const int blocks = combine_blocks(B, s, H), most = kCombineCtasPerSm * sm_count();
-    e = launch_pdl(dec_combine_kernel, dim3(blocks < most ? blocks : most), dim3(kCombineThreads), kCombineSmem, strm,
-                   (const int32_t *)da.plan, (const int *)cflags, (const float *)da.part_o, (const float *)da.part_lse2,
-                   B, s, H, (bf16 *)out_latent, out_lse, da.err, da.limit_ns);
+    const long long rows = (long long)B * s * H, most = 8ll * sm_count();
+    const bool few = rows <= kD4FewRows && ranges >= (long long)kD4ManyPieces * B;
+    const long long blocks = few ? rows * 4 : (rows + kD4CombineWarps - 1) / kD4CombineWarps;
+    e = launch_pdl(few ? dec4_combine_kernel<true> : dec4_combine_kernel<false>,
+                   dim3((unsigned)(blocks < most ? blocks : most)), dim3(32 * kD4CombineWarps), 0, strm,
+                   (const int32_t *)da.plan, (const float *)da.part_o, (const float *)da.part_lse2, B, s, H,
+                   (bf16 *)out_latent, out_lse);
     count_launch();
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

@@ -25,6 +25,9 @@
 //     memory into registers one page ahead, and widen them into the tile layout
 //     when its stage is free.  No copy of the codes passes through shared
 //     memory, which the three stages fill.
+//     Each register is loaded again in place right after its use and touched a page
+//     later: a copy of one in between would wait for its load (293 against 223 us on
+//     128 sequences x 128 heads x 4,096 tokens).
 //   - Warp 0 walks the range's tile list and publishes {page, sequence, tile}
 //     entries in shared memory (and warms L2), so that no other warp holds the
 //     walk's state: the loops of all roles together stay small, because the
@@ -43,9 +46,9 @@
 // Rows past a sequence's end get logit -inf, so weight 0; any pattern a page
 // can hold is finite, so their latents add exactly 0 and need no zeroing.
 //
-// Work split, partial results and the combine are the bf16 decode's
-// (plan_range, dec_combine_kernel); every merge is the combine's.  Every wait
-// is bounded; one that gives up sets MLA_DEVERR_TIMEOUT and the CTA unwinds.
+// Work split and partial results are the bf16 decode's (plan_range); every cut
+// sequence is merged by dec4_combine_kernel.  Every wait is bounded; one that gives
+// up sets MLA_DEVERR_TIMEOUT and the CTA unwinds.
 #pragma once
 
 #include "dec_common.cuh"
@@ -63,6 +66,7 @@ constexpr int kD4OffList = kD4OffEpi + 4 * 16 * 128;
 constexpr int kD4List = 16;                       // published tile entries
 constexpr int kD4OffBar = kD4OffList + kD4List * 16;
 constexpr int kD4Smem = kD4OffBar + 256 + 1024;   // + alignment slack
+constexpr int kD4MinTiles = 2;                    // tiles of a range, where there are enough
 constexpr int kD4Ahead = 6;                       // tiles published ahead of the one being widened
 constexpr uint32_t kD4TmO = 16u << 16, kD4TmQ = 128;
 
@@ -71,7 +75,7 @@ struct Dec4Args {
     const uint8_t *codes, *scales;    // [num_blocks][64][288], [num_blocks][64][36]
     const int32_t *block_table, *seq_lens;
     int32_t *plan;                    // written by CTA 0 for the combine
-    int *work;                        // raised by the number of sequences the combine finishes
+    int *work;                        // (plan_range counts the sequences to merge here)
     bf16 *out;
     float *out_lse;
     float *part_o, *part_lse2;        // [2*ranges][s*H][512], [2*ranges][s*H]
@@ -89,6 +93,26 @@ struct __align__(16) Dec4Tile {
 };
 constexpr int kD4First = 1 << 30, kD4Last = 1 << 29, kD4Complete = 1 << 28, kD4Tt = (1 << 28) - 1;
 
+// The waits of this kernel poll in a few instructions and come here every 256
+// polls: out of line, because the code of a wait that does not end is never run and
+// would sit between the loops' own instructions in the instruction cache.  Returns
+// the time the wait started (0 before the first call), or ~0 to give up: *abort is
+// set, or the limit has passed (then the error bit and *abort are set).
+__device__ __noinline__ uint64_t d4_wait_tick(uint64_t t0, volatile int *abort, uint32_t *err, uint64_t limit_ns)
+{
+    const uint64_t now = sm100::globaltimer_ns();
+    if (t0 == 0) return *abort ? ~0ull : now;
+    if (*abort) return ~0ull;
+    if (now - t0 > limit_ns) {
+        set_error(err, MLA_DEVERR_TIMEOUT);
+        *abort = 1;
+        return ~0ull;
+    }
+    return t0;
+}
+
+#define D4_RARE(x) __builtin_expect(!!(x), 0)
+
 __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec4Args a)
 {
     extern __shared__ uint8_t d4_smem_raw[];
@@ -98,7 +122,6 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
     uint64_t *cv_full = bars;         // [3] stage widened (8 converter warps)
     uint64_t *kv_empty = bars + 3;    // [3] P C of the stage done
     uint64_t *s_full = bars + 6;      // [2] S(k) in buffer k % 2
-    uint64_t *s_free = bars + 8;      // [2] buffer read (4 softmax warps)
     uint64_t *p_full = bars + 10;     // [2] P(k) written and O rescaled (4 softmax warps)
     uint64_t *mma_done = bars + 12;   // the issuer's last MMAs done (teardown)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 13);
@@ -119,7 +142,6 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
         }
         for (int i = 0; i < 2; ++i) {
             sm100::mbar_init(&s_full[i], 1);
-            sm100::mbar_init(&s_free[i], 4);
             sm100::mbar_init(&p_full[i], 4);
         }
         sm100::mbar_init(mma_done, 1);
@@ -147,23 +169,34 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
     }
     const unsigned long long lim = a.limit_ns;
     const unsigned long long drain_lim = lim > 200000000ull ? lim : 200000000ull;
-    // the entry of tile k, once it is published
+    // Bounded waits of one thread: until *cnt >= target, and for a barrier's phase.
+    // (A count's wait has no fence: what it covers lies in shared memory and is read
+    // with volatile loads, which this thread's accesses stay in order with, and a
+    // fence would also wait for the page loads in flight.)
+    auto count_wait = [&](volatile int *cnt, int target) -> bool {
+        uint64_t t0 = 0;
+        for (uint32_t i = 1; *cnt < target; ++i)
+            if (D4_RARE((i & 255u) == 0) && (t0 = d4_wait_tick(t0, abort_flag, a.err, lim)) == ~0ull) return false;
+        return true;
+    };
+    auto bar_wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        const uint32_t at = sm100::smem_u32(bar);
+        uint64_t t0 = 0;
+        for (uint32_t i = 1; !sm100::mbar_test(at, parity); ++i)
+            if (D4_RARE((i & 255u) == 0) && (t0 = d4_wait_tick(t0, abort_flag, a.err, lim)) == ~0ull) return false;
+        return true;
+    };
+    // Warp-uniform: every lane polls, one vote (no shuffle through the queue that the
+    // warp's stores and loads are in).
+    auto phase_wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, bar_wait(bar, parity));
+    };
+    // the entry of tile k, once it is published (every thread for itself)
     auto tile_at = [&](int k, Dec4Tile &t) -> bool {
-        if (*listed <= k) {
-            const uint64_t t0 = sm100::globaltimer_ns();
-            for (uint32_t i = 1; *listed <= k; ++i)
-                if ((i & 255u) == 0) {
-                    if (*abort_flag) return false;
-                    if (sm100::globaltimer_ns() - t0 > lim) {
-                        set_error(a.err, MLA_DEVERR_TIMEOUT);
-                        *abort_flag = 1;
-                        return false;
-                    }
-                }
-        }
-        __threadfence_block();
-        const int4 v = *reinterpret_cast<const int4 *>(&list[k % kD4List]);
-        t.page = v.x; t.seq = v.y; t.tt = v.z; t.seg = v.w;
+        if (!count_wait(listed, k + 1)) return false;
+        const uint32_t e = sm100::smem_u32(&list[k % kD4List]);
+        asm volatile("ld.volatile.shared.v4.s32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(t.page), "=r"(t.seq), "=r"(t.tt), "=r"(t.seg) : "r"(e) : "memory");
         return true;
     };
 
@@ -175,7 +208,11 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
         TileIter it;
         it.init(a.seq_lens, a.max_blocks, a.B, lo, hi, rplan[2], rplan[3], rplan[5]);
         for (; it.ok; it.advance()) {
-            if (!wait_count(cvt_at, it.k - kD4Ahead, abort_flag, a.err, lim)) break;
+            // (a sleeping poll: nothing waits for the entry yet, and the slots a busy
+            // one would take belong to the other warps; it ends with the converters'
+            // own bounded waits)
+            while (*cvt_at < it.k - kD4Ahead && !*abort_flag) __nanosleep(200);
+            if (__any_sync(0xffffffffu, *abort_flag)) break;
             if (lane == 0) {
                 int page = __ldcg(a.block_table + (long long)it.seq * a.max_blocks + it.tt);
                 if (page < 0 || page >= a.num_blocks) {
@@ -205,23 +242,12 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
             const uint32_t idesc_s = sm100::idesc_bf16(kGroupRows, kBlock, 0, 0);
             const uint32_t idesc_o = sm100::idesc_bf16(kGroupRows, 256, 0, 1);
             const uint32_t st0 = sm100::smem_u32(smem);
+            // S(k)'s buffer is free: P C(k - 2) was issued before it and waited for the
+            // softmax of tile k - 2
             auto issue_s = [&](int k, const Dec4Tile &t) -> bool {
                 const int st = k % kD4Stages, b = k & 1;
-                if (t.tt & kD4First) {   // its queries are in TMEM
-                    const uint64_t t0 = sm100::globaltimer_ns();
-                    for (uint32_t i = 1; *q_cnt < 4 * (t.seg + 1); ++i)
-                        if ((i & 255u) == 0) {
-                            if (*abort_flag) return false;
-                            if (sm100::globaltimer_ns() - t0 > lim) {
-                                set_error(a.err, MLA_DEVERR_TIMEOUT);
-                                *abort_flag = 1;
-                                return false;
-                            }
-                        }
-                    __threadfence_block();
-                }
-                if (!sm100::mbar_wait(&cv_full[st], (k / kD4Stages) & 1, abort_flag, a.err, lim)) return false;
-                if (k >= 2 && !sm100::mbar_wait(&s_free[b], ((k >> 1) - 1) & 1, abort_flag, a.err, lim)) return false;
+                if (D4_RARE(t.tt & kD4First) && !count_wait(q_cnt, 4 * (t.seg + 1))) return false;
+                if (!bar_wait(&cv_full[st], (k / kD4Stages) & 1)) return false;
                 sm100::tc_fence_after();
                 const uint64_t kd = sm100::desc_kmajor(st0 + st * kD4Stage, 128, sm100::kSw128);
 #pragma unroll 1
@@ -235,7 +261,7 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
             };
             auto issue_o = [&](int k, uint32_t acc0) -> bool {
                 const int st = k % kD4Stages;
-                if (!sm100::mbar_wait(&p_full[k & 1], (k >> 1) & 1, abort_flag, a.err, lim)) return false;
+                if (!bar_wait(&p_full[k & 1], (k >> 1) & 1)) return false;
                 sm100::tc_fence_after();
                 const uint64_t vd = sm100::desc_mnmajor_sw128(st0 + st * kD4Stage, kD4Chunk);
                 const uint64_t pd = sm100::desc_kmajor(st0 + st * kD4Stage + kD4PChunk, 128, sm100::kSw128);
@@ -267,6 +293,13 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
             sm100::umma_commit(mma_done);
         }
         __syncwarp();
+    } else if (warp == 3) {
+        // the first segment's queries into L2, ahead of the warps that read them
+        if (lane < 8) {
+            const int g0 = group * kGroupRows + 8 * lane, nr = min(8, rows_per_seq - g0);
+            if (nr > 0)
+                sm100::bulk_prefetch_l2(a.q_abs + ((long long)rplan[2] * rows_per_seq + g0) * kRow, nr * kRow * 2);
+        }
     } else if (warp >= 8) {
         // ------------------------------------------------ 4-bit -> bf16
         // Thread (r, p) = (ct / 4, ct % 4) takes, of row r and each 128-column
@@ -315,7 +348,7 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
             uint32_t n0 = 0, n1 = 0, n8 = 0;
             if (ok && more) { n0 = __ldcg(sc + p); n1 = __ldcg(sc + 4 + p); n8 = __ldcg(sc + 8); }
             if (ok && k >= kD4Stages)
-                ok = sm100::warp_wait(&kv_empty[st], ((k / kD4Stages) - 1) & 1, abort_flag, a.err, lim);
+                ok = phase_wait(&kv_empty[st], ((k / kD4Stages) - 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (k == a.stall_tile) continue;   // test hook: this tile never becomes full
@@ -393,6 +426,7 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
             }
         };
         float m_run = -INFINITY, l_run = 0.f;
+        const bool any_row = group * kGroupRows + 16 * qd < rows_per_seq;
         int nvis = 0;
         Dec4Tile t;
         bool ok = tile_at(0, t);
@@ -400,15 +434,20 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
         for (int k = 0; ok && k < ntile; ++k) {
             const int b = k & 1, st = k % kD4Stages;
             if (k > 0) ok = tile_at(k, t);
-            if (ok && (t.tt & kD4First)) {
+            if (D4_RARE(ok && (t.tt & kD4First))) {
                 m_run = -INFINITY;
                 l_run = 0.f;
                 // query tq of a sequence of length L sees positions j <= L - s + tq
                 nvis = seq_len_clamped(a.seq_lens, t.seq, a.max_blocks) - a.s + tq + 1;
             }
-            if (ok) ok = sm100::warp_wait(&s_full[b], (k >> 1) & 1, abort_flag, a.err, lim);
+            if (ok) ok = phase_wait(&s_full[b], (k >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+            if (!any_row && !(t.tt & kD4Last)) {   // no row of this quarter is stored: whatever P holds will do
+                if (lane == 0) sm100::mbar_arrive(&p_full[b]);
+                __syncwarp();
+                continue;
+            }
             sm100::tc_fence_after();
             float x[32];
             {
@@ -417,12 +456,9 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
                 sm100::tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(sv[c]);
-                sm100::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) sm100::mbar_arrive(&s_free[b]);
             }
             const int left = nvis - (t.tt & kD4Tt) * kBlock - (srow ? 0 : 32);   // visible of these 32 columns
-            if (left < 32) {
+            if (D4_RARE(left < 32)) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                     if (c >= left) x[c] = -INFINITY;
@@ -437,10 +473,10 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
             const bool rescale = grown && m_run != -INFINITY;
             const float m_new = grown ? mt : m_run;
             const float corr = rescale ? ex2(m_run - m_new) : (grown ? 0.f : 1.f);
-            if (__any_sync(0xffffffffu, rescale)) {
+            if (D4_RARE(__any_sync(0xffffffffu, rescale))) {
                 // O holds this segment's tiles up to k - 1: let them retire, then
                 // scale the O lanes (S(k + 1) may be using the other half)
-                ok = sm100::warp_wait(&kv_empty[(k - 1) % kD4Stages], ((k - 1) / kD4Stages) & 1, abort_flag, a.err, lim);
+                ok = phase_wait(&kv_empty[(k - 1) % kD4Stages], ((k - 1) / kD4Stages) & 1);
                 if (!ok) break;
                 sm100::tc_fence_after();
                 const float f = rescale ? corr : 1.f;
@@ -489,7 +525,7 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
             if (k + 1 < ntile) ok = tile_at(k + 1, nx);
             ok = __all_sync(0xffffffffu, ok);
             if (ok && nx.seq >= 0) write_q(nx.seq);
-            ok = ok && sm100::warp_wait(&kv_empty[st], (k / kD4Stages) & 1, abort_flag, a.err, lim);
+            ok = ok && phase_wait(&kv_empty[st], (k / kD4Stages) & 1);
             if (!ok) break;
             sm100::tc_fence_after();
             const float l_tot = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
@@ -561,6 +597,127 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
         sm100::warp_wait(mma_done, 0, &no_abort, a.err, drain_lim);
         sm100::tc_fence_after();
         sm100::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ combine
+// Sequences cut by range ends are merged by log-sum-exp; sequences one range
+// finished are already in place; query rows with no visible key get a zero
+// latent and lse = -inf.  Only the sequences plan_range lists are visited.
+//   kFew = false: one warp per row, all 512 columns, two pieces' loads in flight.
+//   kFew = true, where a sequence can be cut into kD4ManyPieces pieces or more and
+//     the batch has few rows: one CTA per (row, 128 columns), its eight warps taking
+//     the pieces eight by eight in turn, eight loads in flight each; their sums are
+//     added in warp order.  One sequence of 16 heads and 32,768 tokens (148 pieces):
+//     the call takes 31 us so, 50 us with a warp per row and 128 columns; 4 x 128
+//     heads x 2,000 tokens (16 pieces): 38 us so, 27 us with a warp per row.
+// The weights 2^(lse2_i - max) are kept per warp in shared memory; a warp sums its
+// pieces in range order, so the bits do not change from run to run.
+constexpr int kD4CombineWarps = 8;
+constexpr int kD4ManyPieces = 64, kD4FewRows = 512;
+
+template <bool kFew>
+__global__ void __launch_bounds__(32 * kD4CombineWarps)
+dec4_combine_kernel(const int32_t *plan, const float *part_o, const float *part_lse2, int B, int s, int H,
+                    bf16 *__restrict__ out, float *__restrict__ out_lse)
+{
+    constexpr int kQuads = kFew ? 1 : 4;      // 128-column quarters of a warp
+    constexpr int kAhead = 8 / kQuads;        // pieces in flight
+    __shared__ float weight[kD4CombineWarps][kMaxRanges];
+    __shared__ float4 sums[kFew ? kD4CombineWarps : 1][32];
+    // what the decode kernel wrote is read only after the wait and only through L2
+    sm100::pdl_wait();
+    const int qv = __ldcg(plan), pw = __ldcg(plan + 3), nlist = __ldcg(plan + 5 + B);
+    const int4 *list = reinterpret_cast<const int4 *>(plan + plan_list_off(B));
+    const unsigned rows = s * H, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned items = nlist * rows * (kFew ? 4 : 1);
+    const unsigned step = kFew ? gridDim.x : gridDim.x * kD4CombineWarps;
+    for (unsigned it = kFew ? blockIdx.x : blockIdx.x * kD4CombineWarps + warp; it < items; it += step) {
+        const unsigned part = kFew ? it & 3 : 0, line = kFew ? it >> 2 : it;
+        const unsigned li = line / rows, row = line - li * rows;
+        const int4 seq = __ldcg(list + li);
+        const int b = seq.x, va = seq.y, tb = seq.z, L = seq.w;
+        const long long orow = (long long)b * rows + row;
+        const int col = 128 * part + 4 * lane;   // and, of one warp per row, 128 columns on, ..
+        const bool writes = !kFew || warp == 0;
+        // the ranges holding the sequence's first and last tiles; the piece in range
+        // c0 is that range's first segment only if the range starts with the sequence
+        // (slot 2 c0), else its last (2 c0 + 1); every later piece is its range's
+        // first segment (slot 2 c)
+        const int c0 = tb > 0 ? (va + pw) / qv : 0, c1 = tb > 0 ? (va + pw + tb - 1) / qv : 0;
+        const bool visible = L - s + (int)(row / H) + 1 > 0;   // query row / H sees some key
+        if (!visible || tb == 0) {   // (the same for every warp of a kFew CTA)
+            if (writes) {
+#pragma unroll
+                for (int e = 0; e < kQuads; ++e)
+                    *reinterpret_cast<uint2 *>(out + orow * kDc + col + 128 * e) = make_uint2(0, 0);
+                if (part == 0 && lane == 0 && out_lse) out_lse[orow] = -INFINITY;
+            }
+            continue;
+        }
+        const int n = c1 - c0 + 1, slot0 = 2 * c0 + (c0 * qv < va ? 1 : 0);
+        auto row_of = [&](int i) { return (long long)(i == 0 ? slot0 : 2 * (c0 + i)) * rows + row; };
+        float M = -INFINITY;
+        for (int i = lane; i < n; i += 32) {
+            const float l2 = __ldcg(part_lse2 + row_of(i));
+            weight[warp][i] = l2;
+            M = fmaxf(M, l2);
+        }
+        M = warp_max(M);
+        float den = 0.f;
+        for (int i = lane; i < n; i += 32) {
+            const float l2 = weight[warp][i], w = l2 == -INFINITY ? 0.f : exp2f(l2 - M);
+            weight[warp][i] = w;
+            den += w;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+        __syncwarp();
+        float4 acc[kQuads] = {};
+        for (int i0 = kFew ? warp * kAhead : 0; i0 < n; i0 += kFew ? kD4CombineWarps * kAhead : kAhead) {
+            float4 v[kAhead][kQuads];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+                for (int e = 0; e < kQuads; ++e)
+                    v[j][e] = i0 + j < n ? __ldcg(reinterpret_cast<const float4 *>(part_o + row_of(i0 + j) * kDc + col + 128 * e))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const float w = i0 + j < n ? weight[warp][i0 + j] : 0.f;
+#pragma unroll
+                for (int e = 0; e < kQuads; ++e) {
+                    acc[e].x = fmaf(w, v[j][e].x, acc[e].x);
+                    acc[e].y = fmaf(w, v[j][e].y, acc[e].y);
+                    acc[e].z = fmaf(w, v[j][e].z, acc[e].z);
+                    acc[e].w = fmaf(w, v[j][e].w, acc[e].w);
+                }
+            }
+        }
+        if (kFew) {
+            sums[warp][lane] = acc[0];
+            __syncthreads();
+            if (warp == 0)
+                for (int w = 1; w < kD4CombineWarps; ++w) {
+                    const float4 x = sums[w][lane];
+                    acc[0].x += x.x;
+                    acc[0].y += x.y;
+                    acc[0].z += x.z;
+                    acc[0].w += x.w;
+                }
+        }
+        if (writes) {
+            const float inv = den > 0.f ? 1.f / den : 0.f;
+#pragma unroll
+            for (int e = 0; e < kQuads; ++e)
+                *reinterpret_cast<uint2 *>(out + orow * kDc + col + 128 * e) =
+                    make_uint2(pack_bf162(acc[e].x * inv, acc[e].y * inv), pack_bf162(acc[e].z * inv, acc[e].w * inv));
+            if (part == 0 && lane == 0 && out_lse) out_lse[orow] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
+        }
+        if (kFew)
+            __syncthreads();   // the sums are read
+        else
+            __syncwarp();      // the weights are read
     }
 }
 
