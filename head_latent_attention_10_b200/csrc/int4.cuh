@@ -42,12 +42,38 @@ __device__ __forceinline__ uint32_t int4_scale_byte(float amax)
 
 __device__ __forceinline__ float int4_scale(uint32_t b) { return __uint_as_float((b << 20) + (112u << 23)); }
 
-// The code of x: 8 + x / s (fp32 quotient) rounded to nearest-even, the
-// magnitude clamped to 7.
-__device__ __forceinline__ uint32_t int4_code(float x, float s)
+// The code of a bf16 x under scale s in the low four bits of the result, above them
+// the constant kInt4CodeBits: 8 + x / s rounded to nearest-even, |x| <= 7.5 s; inv_s
+// is 1 / s in fp32.  x * inv_s is within 2^-24 of the quotient, relative.  With
+// x = X 2^a (X < 256) and s = S 2^b (8 <= S < 16), a quotient below 8 that is not a
+// tie k + 1/2 is at least 1/480 away from one, so the sum with 192, which the one
+// rounding of the multiply-add takes to a multiple of 2^-16, restores the ties and
+// moves nothing across them.  The addition rounds to an integer: 1.5 2^23 + 8 - 192 +
+// the sum lies where fp32 has spacing 1.
+constexpr uint32_t kInt4CodeBits = 0x4B400000u;   // 1.5 2^23
+__device__ __forceinline__ uint32_t int4_code(float x, float inv_s)
 {
-    return (uint32_t)(8 + (int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -7.f), 7.f));
+    return __float_as_uint(__fadd_rn(__fmaf_rn(x, inv_s, 192.f), 12582912.f + 8.f - 192.f));
 }
+
+// A pair of bf16 values without NaN: a NaN becomes 0.
+__device__ __forceinline__ uint32_t int4_known(uint32_t h)
+{
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&h);
+    return h & __heq2_mask(x, x);
+}
+
+// A pair limited to +-7 s (7 bits: a bf16 value), where the scale is the format's
+// largest: elsewhere no value of the group is beyond 7.5 s.
+__device__ __forceinline__ uint32_t int4_limit(uint32_t h, float s)
+{
+    const __nv_bfloat162 l = __float2bfloat162_rn(7.f * s), x = *reinterpret_cast<const __nv_bfloat162 *>(&h);
+    const __nv_bfloat162 y = __hmax2(__hmin2(x, l), __hneg2(l));
+    return *reinterpret_cast<const uint32_t *>(&y);
+}
+
+__device__ __forceinline__ float int4_low(uint32_t h) { return __uint_as_float(h << 16); }
+__device__ __forceinline__ float int4_high(uint32_t h) { return __uint_as_float(h & 0xFFFF0000u); }
 
 // Eight codes (one word) and their scale byte -> 8 bf16 values.  A nibble u
 // OR-ed into bits 6..3 of the bf16 pattern of 16.0 is 16 + u, and
@@ -99,65 +125,86 @@ append_latent_int4_kernel(const bf16 *__restrict__ c_kv, const bf16 *__restrict_
     const int lane = threadIdx.x & 31;
     if (warp >= T) return;
     const int p = pos[warp];
-    const long long slot = cache_slot(block_table, num_seqs, max_blocks, num_blocks, seq_idx[warp], p,
-                                      lane == 0 ? err : nullptr);
-    if (slot < 0) return;
     uint4 v[2];
     __nv_bfloat162 kr;
     latent_row_lanes(c_kv, k_rope, warp, p, lane, rope, norm_w, eps, v[0], v[1], kr);
-    auto known = [](float x) { return x == x ? x : 0.f; };
+    const long long slot = cache_slot(block_table, num_seqs, max_blocks, num_blocks, seq_idx[warp], p,
+                                      lane == 0 ? err : nullptr);
+    if (slot < 0) return;
     uint8_t *crow = codes + slot * kInt4Codes, *srow = scales + slot * kInt4Scales;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v[half]);
-        float x[8], am = 0.f;
+        uint32_t h[4] = {int4_known(v[half].x), int4_known(v[half].y), int4_known(v[half].z), int4_known(v[half].w)};
+        uint32_t am = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __bfloat1622float2(h[i]);
-            x[2 * i] = known(f.x);
-            x[2 * i + 1] = known(f.y);
-            am = fmaxf(am, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+        for (int i = 0; i < 4; ++i) am = __vmaxu2(am, h[i] & 0x7FFF7FFFu);
+        am = __vmaxu2(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        const uint32_t b = int4_scale_byte(int4_low(max(am & 0xFFFFu, am >> 16)));
+        const float s = int4_scale(b), inv = __frcp_rn(s);
+        if (b == 255) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = int4_limit(h[i], s);
         }
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-        const uint32_t b = int4_scale_byte(am);
-        const float s = int4_scale(b);
         uint32_t w = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w |= int4_code(x[2 * i], s) << (4 * i) | int4_code(x[2 * i + 1], s) << (16 + 4 * i);
+            w += ((int4_code(int4_low(h[i]), inv) - kInt4CodeBits) << (4 * i)) +
+                 ((int4_code(int4_high(h[i]), inv) - kInt4CodeBits) << (16 + 4 * i));
         reinterpret_cast<uint32_t *>(crow)[32 * half + lane] = w;
         if ((lane & 1) == 0) srow[16 * half + (lane >> 1)] = (uint8_t)b;
     }
-    const float2 f = __bfloat1622float2(kr);
-    const float x0 = known(f.x), x1 = known(f.y);
-    float am = fmaxf(fabsf(x0), fabsf(x1));
+    uint32_t h = int4_known(*reinterpret_cast<const uint32_t *>(&kr));
+    uint32_t am = h & 0x7FFF7FFFu;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-    const uint32_t b = int4_scale_byte(am);
-    const float s = int4_scale(b);
+    for (int o = 1; o < 8; o <<= 1) am = __vmaxu2(am, __shfl_xor_sync(0xffffffffu, am, o));
+    const uint32_t b = int4_scale_byte(int4_low(max(am & 0xFFFFu, am >> 16)));
+    const float s = int4_scale(b), inv = __frcp_rn(s);
+    if (b == 255) h = int4_limit(h, s);
     const int i = lane & 3;   // the pair's place in its word
-    uint32_t w = int4_code(x0, s) << (4 * i) | int4_code(x1, s) << (16 + 4 * i);
+    uint32_t w = ((int4_code(int4_low(h), inv) - kInt4CodeBits) << (4 * i)) +
+                 ((int4_code(int4_high(h), inv) - kInt4CodeBits) << (16 + 4 * i));
     w |= __shfl_xor_sync(0xffffffffu, w, 1);
     w |= __shfl_xor_sync(0xffffffffu, w, 2);
     if (i == 0) reinterpret_cast<uint32_t *>(crow + kDc / 2)[lane >> 2] = w;
     if ((lane & 7) == 0) srow[kDc / kInt4Group + (lane >> 3)] = (uint8_t)b;
 }
 
-// Rows at T (sequence, position) places, widened to bf16: thread = one
-// 8-value unit of one row.  A place whose slot is invalid gives a row of
-// zeros and an error bit.
-__global__ void __launch_bounds__(256)
-gather_latent_int4_kernel(const Int4Rows rows, int num_blocks, const int32_t *__restrict__ seq_idx,
-                          const int32_t *__restrict__ pos, int T, const int32_t *__restrict__ block_table,
-                          int num_seqs, int max_blocks, bf16 *__restrict__ out, uint32_t *err)
+// Rows at T (sequence, position) places, widened to bf16.  Thread = one 8-value
+// unit of a row, of four rows, whose loads are in flight together; neighbours'
+// 16-byte stores touch.  A place whose slot is invalid gives a row of zeros and an
+// error bit.
+constexpr int kInt4GatherRows = 4, kInt4GatherThreads = kRow / 8;
+
+__global__ void __launch_bounds__(kInt4GatherThreads)
+gather_latent_int4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int num_blocks,
+                          const int32_t *__restrict__ seq_idx, const int32_t *__restrict__ pos, int T,
+                          const int32_t *__restrict__ block_table, int num_seqs, int max_blocks,
+                          bf16 *__restrict__ out, uint32_t *err)
 {
-    constexpr int kUnits = kRow / 8;
-    const long long units = (long long)T * kUnits;
-    for (long long w = (long long)blockIdx.x * blockDim.x + threadIdx.x; w < units; w += (long long)gridDim.x * blockDim.x) {
-        const int t = (int)(w / kUnits), c = (int)(w % kUnits);
-        const long long slot = cache_slot(block_table, num_seqs, max_blocks, num_blocks, seq_idx[t], pos[t],
-                                          c == 0 ? err : nullptr);
-        reinterpret_cast<uint4 *>(out)[w] = slot < 0 ? make_uint4(0, 0, 0, 0) : rows.unit(slot, c);
+    __shared__ long long slots[kInt4GatherRows];
+    const long long t0 = (long long)blockIdx.x * kInt4GatherRows;
+    const int c = threadIdx.x;
+    if (c < kInt4GatherRows)
+        slots[c] = t0 + c < T ? cache_slot(block_table, num_seqs, max_blocks, num_blocks, seq_idx[t0 + c], pos[t0 + c],
+                                           err) : -1;
+    __syncthreads();
+    uint32_t w[kInt4GatherRows], b[kInt4GatherRows];
+#pragma unroll
+    for (int e = 0; e < kInt4GatherRows; ++e) {
+        const long long slot = slots[e];
+        w[e] = 0x88888888u;   // eight codes of value 0
+        b[e] = 0;
+        if (slot >= 0) {
+            w[e] = reinterpret_cast<const uint32_t *>(codes + slot * kInt4Codes)[c];
+            b[e] = scales[slot * kInt4Scales + (c >> 1)];
+        }
+    }
+    uint4 *o = reinterpret_cast<uint4 *>(out + t0 * kRow) + c;
+#pragma unroll
+    for (int e = 0; e < kInt4GatherRows; ++e) {
+        __nv_bfloat162 s2, m24s2;
+        int4_scale2(b[e], s2, m24s2);
+        if (t0 + e < T) o[e * kInt4GatherThreads] = int4_widen8(w[e], s2, m24s2);
     }
 }
 

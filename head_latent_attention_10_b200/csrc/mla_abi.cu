@@ -908,13 +908,9 @@ mla_status_t mla_gather_latent_int4(const mla_dims_t *dims, const void *codes, c
     if (!codes || !scales || !seq_idx || !pos || !block_table || !rows) return MLA_ERR_INVALID_ARG;
     if (!aligned16(codes) || !aligned16(scales) || !aligned16(rows)) return MLA_ERR_INVALID_ARG;
     if (!int4_sizes_ok(1, 1, 1, max_blocks)) return MLA_ERR_UNSUPPORTED;
-    const int sms = sm_count();
-    if (sms <= 0) return MLA_ERR_CUDA;
-    long long blocks = ((long long)T * (kRow / 8) + 255) / 256;
-    if (blocks > 8ll * sms) blocks = 8ll * sms;
-    gather_latent_int4_kernel<<<(int)blocks, 256, 0, as_stream(stream)>>>(
-        Int4Rows{(const uint8_t *)codes, (const uint8_t *)scales}, num_blocks, seq_idx, pos, T, block_table, num_seqs,
-        max_blocks, (bf16 *)rows, err_word);
+    gather_latent_int4_kernel<<<(T - 1) / kInt4GatherRows + 1, kInt4GatherThreads, 0, as_stream(stream)>>>(
+        (const uint8_t *)codes, (const uint8_t *)scales, num_blocks, seq_idx, pos, T, block_table, num_seqs, max_blocks,
+        (bf16 *)rows, err_word);
     count_launch();
     return cuda_status(cudaGetLastError());
 }

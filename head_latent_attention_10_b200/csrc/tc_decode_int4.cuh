@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
     auto phase_wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, bar_wait(bar, parity));
     };
-    // the entry of tile k, once it is published (every thread for itself)
+    // the entry of tile k, once it is published (every thread for itself: where
+    // lanes must agree, the caller votes before its next warp-wide step)
     auto tile_at = [&](int k, Dec4Tile &t) -> bool {
         if (!count_wait(listed, k + 1)) return false;
         const uint32_t e = sm100::smem_u32(&list[k % kD4List]);
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
         // place and touches it only a page later: a copy or a select on it there
         // would wait for the load
         Dec4Tile t;
-        bool ok = tile_at(0, t);
+        bool ok = __all_sync(0xffffffffu, tile_at(0, t));
         uint4 q[4];
         uint2 c8;
         uint32_t s0, s1, s8;
@@ -347,8 +348,8 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
             const uint32_t *sc = words_of(t.page);
             uint32_t n0 = 0, n1 = 0, n8 = 0;
             if (ok && more) { n0 = __ldcg(sc + p); n1 = __ldcg(sc + 4 + p); n8 = __ldcg(sc + 8); }
-            if (ok && k >= kD4Stages)
-                ok = phase_wait(&kv_empty[st], ((k / kD4Stages) - 1) & 1);
+            if (k >= kD4Stages)   // (whatever this lane's ok: the wait votes)
+                ok = phase_wait(&kv_empty[st], ((k / kD4Stages) - 1) & 1) && ok;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (k == a.stall_tile) continue;   // test hook: this tile never becomes full
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
         const bool any_row = group * kGroupRows + 16 * qd < rows_per_seq;
         int nvis = 0;
         Dec4Tile t;
-        bool ok = tile_at(0, t);
+        bool ok = __all_sync(0xffffffffu, tile_at(0, t));
         if (ok) write_q(t.seq);
         for (int k = 0; ok && k < ntile; ++k) {
             const int b = k & 1, st = k % kD4Stages;
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
                 // query tq of a sequence of length L sees positions j <= L - s + tq
                 nvis = seq_len_clamped(a.seq_lens, t.seq, a.max_blocks) - a.s + tq + 1;
             }
-            if (ok) ok = phase_wait(&s_full[b], (k >> 1) & 1);
+            ok = phase_wait(&s_full[b], (k >> 1) & 1) && ok;   // (whatever this lane's ok: the wait votes)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (!any_row && !(t.tt & kD4Last)) {   // no row of this quarter is stored: whatever P holds will do
