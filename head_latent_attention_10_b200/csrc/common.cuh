@@ -79,6 +79,12 @@ __device__ __forceinline__ float rms_inv(float ss, float eps)
     return 1.0f / sqrtf(ss / (float)kDc + eps);
 }
 
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    __half2 t = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&t);
+}
+
 __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi)
 {
     __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);

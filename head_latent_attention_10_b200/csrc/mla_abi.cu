@@ -436,7 +436,7 @@ mla_status_t run_simple_decode(const mla_dims_t *dims, const void *q_abs, const 
 
 // The prefill over cache rows read through `cache` (argument checks are the
 // caller's).
-template <class Rows>
+template <bool kHalfV, class Rows>
 mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void *q_rope, const int32_t *q_pos,
                          const void *w_uk, const void *w_uv, const Rows &cache, int num_blocks,
                          const int32_t *block_table, int max_blocks, const int32_t *seq_lens, int B, int s,
@@ -450,7 +450,7 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
     if (rows_total > (1ll << 31) - 1 || (long long)B * s * H > (1ll << 31) - 1) return MLA_ERR_UNSUPPORTED;
     const int M = (int)rows_total;
     char *ws = (char *)workspace;
-    uint32_t *err = (uint32_t *)ws;
+    uint32_t *err = (uint32_t *)ws, *max_bits = err + 2;
     bf16 *rows = (bf16 *)(ws + w.off_rows), *q_rot = (bf16 *)(ws + w.off_qr);
     bf16 *kc = (bf16 *)(ws + w.off_kc), *vc = (bf16 *)(ws + w.off_vc);
     const long long cap_blocks = (long long)max_blocks * kBlock;
@@ -482,23 +482,29 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
         pm.kc = mkc;
         pm.vc = mvc;
     }
-    if (cudaMemsetAsync(err, 0, sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
+    if (cudaMemsetAsync(err, 0, (kHalfV ? 4 : 1) * sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
     {
         const long long work = rows_total * (kRow / 8) + (long long)B * s * (kDr / 2);
         long long blocks = (work + 255) / 256;
         if (blocks > 8ll * sm_count()) blocks = 8ll * sm_count();
-        prefill_prepare_kernel<Rows><<<(int)blocks, 256, 0, strm>>>(cache, num_blocks, block_table, max_blocks,
+        prefill_prepare_kernel<Rows, kHalfV><<<(int)blocks, 256, 0, strm>>>(cache, num_blocks, block_table, max_blocks,
                                                                     seq_lens, B, s, H, w.lpad, l_cap, rows,
                                                                     (const bf16 *)q_rope, q_pos, q_rot,
-                                                                    rope_table(dims), err);
+                                                                    rope_table(dims), (const uint4 *)w_uv,
+                                                                    (long long)H * kDh * kDc / 8, max_bits, err);
         count_launch();
         if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
     }
     if (launch_tc_gemm<256, false, TcEpiTmaStore>(ma, muk, M, H * kDh, kDc, 1, TcEpiTmaStore{}, err, strm, &skc) !=
-            cudaSuccess ||
-        launch_tc_gemm<256, false, TcEpiTmaStore>(ma, muv, M, H * kDh, kDc, 1, TcEpiTmaStore{}, err, strm, &svc) !=
-            cudaSuccess)
+        cudaSuccess)
         return MLA_ERR_CUDA;
+    cudaError_t ve;
+    if constexpr (kHalfV)
+        ve = launch_tc_gemm<256, false, TcEpiTmaStoreHalf>(ma, muv, M, H * kDh, kDc, 1, TcEpiTmaStoreHalf{max_bits},
+                                                           err, strm, &svc);
+    else
+        ve = launch_tc_gemm<256, false, TcEpiTmaStore>(ma, muv, M, H * kDh, kDc, 1, TcEpiTmaStore{}, err, strm, &svc);
+    if (ve != cudaSuccess) return MLA_ERR_CUDA;
     PrefillArgs pa;
     pa.q_nope = (const bf16 *)q_nope;
     pa.q_rot = q_rot;
@@ -510,10 +516,11 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
     pa.scale_log2 = softmax_scale(dims) * kLog2e;
     pa.out_lse = out_lse;
     pa.err = err;
+    pa.max_bits = max_bits;
     pa.limit_ns = kWaitLimitNs;
     static std::atomic<bool> attr_set[kMaxDevices];
-    if (ensure_smem_attr(tc_prefill_kernel, kPfSmem, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
-    tc_prefill_kernel<<<dim3((s + 127) / 128, H, B), kPfThreads, kPfSmem, strm>>>(pm, pa);
+    if (ensure_smem_attr(tc_prefill_kernel<kHalfV>, kPfSmem, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
+    tc_prefill_kernel<kHalfV><<<dim3((s + 127) / 128, H, B), kPfThreads, kPfSmem, strm>>>(pm, pa);
     count_launch();
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
     if (flags & MLA_SYNC_CHECK) {
@@ -819,7 +826,7 @@ mla_status_t mla_prefill(const mla_dims_t *dims, const void *q_nope, const void 
         !aligned16(out))
         return MLA_ERR_INVALID_ARG;
     if (!workspace) return MLA_ERR_WORKSPACE;
-    return run_prefill(dims, q_nope, q_rope, q_pos, w_uk, w_uv, Bf16Rows{(const bf16 *)cache}, num_blocks, block_table,
+    return run_prefill<false>(dims, q_nope, q_rope, q_pos, w_uk, w_uv, Bf16Rows{(const bf16 *)cache}, num_blocks, block_table,
                        max_blocks, seq_lens, B, s, max_seq_len, out, out_lse, workspace, ws_bytes, flags,
                        as_stream(stream));
 }
@@ -970,7 +977,7 @@ mla_status_t mla_prefill_int4(const mla_dims_t *dims, const void *q_nope, const 
     if (!int4_sizes_ok(B, s, dims->num_heads, max_blocks) || max_seq_len > (1ll << 31) - 1 - 127 || B > 65535)
         return MLA_ERR_UNSUPPORTED;
     if (!workspace) return MLA_ERR_WORKSPACE;
-    return run_prefill(dims, q_nope, q_rope, q_pos, w_uk, w_uv,
+    return run_prefill<true>(dims, q_nope, q_rope, q_pos, w_uk, w_uv,
                        Int4Rows{(const uint8_t *)codes, (const uint8_t *)scales}, num_blocks, block_table, max_blocks,
                        seq_lens, B, s, max_seq_len, out, out_lse, workspace, ws_bytes, flags, as_stream(stream));
 }

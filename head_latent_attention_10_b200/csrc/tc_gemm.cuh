@@ -33,6 +33,16 @@ struct GemmSmem {
     static constexpr int TMEM_COLS = BN <= 32 ? 32 : (BN <= 64 ? 64 : (BN <= 128 ? 128 : 256));
 };
 
+// 2^n, |n| <= 126, and the exponent e of TcEpiTmaStoreHalf: a pattern with
+// exponent field x stands for less than 2^(x - 126), so the bound is
+// 2^(9 + x - 126 + y - 126).
+__device__ __forceinline__ float exp2_int(int n) { return __uint_as_float((uint32_t)(127 + n) << 23); }
+__device__ __forceinline__ int half_exponent(const uint32_t *max_bits)
+{
+    const int e = (int)(__ldcg(max_bits) >> 7) + (int)(__ldcg(max_bits + 1) >> 7) - 258;
+    return min(max(e, -126), 126);
+}
+
 template <int BN, bool kBmn, class Epi, bool kAmn = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
@@ -142,6 +152,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
             // [128 rows][128 B] (128-byte swizzle), stored with TMA by one
             // thread: whole lines rather than 32 rows' pieces per instruction
             const int r = q * 32 + lane;
+            const float f = epi.factor();
 #pragma unroll 1
             for (int c = 0; c < BN; c += 32) {
                 uint32_t v[32];
@@ -158,10 +169,10 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
                 for (int u = 0; u < 4; ++u) {
                     const int uu = ((c % 64) / 8) + u;
                     *reinterpret_cast<uint4 *>(chunk + r * 128 + ((uu ^ (r & 7)) << 4)) =
-                        make_uint4(pack_bf162(__uint_as_float(v[8 * u]), __uint_as_float(v[8 * u + 1])),
-                                   pack_bf162(__uint_as_float(v[8 * u + 2]), __uint_as_float(v[8 * u + 3])),
-                                   pack_bf162(__uint_as_float(v[8 * u + 4]), __uint_as_float(v[8 * u + 5])),
-                                   pack_bf162(__uint_as_float(v[8 * u + 6]), __uint_as_float(v[8 * u + 7])));
+                        make_uint4(epi.pack(__uint_as_float(v[8 * u]), __uint_as_float(v[8 * u + 1]), f),
+                                   epi.pack(__uint_as_float(v[8 * u + 2]), __uint_as_float(v[8 * u + 3]), f),
+                                   epi.pack(__uint_as_float(v[8 * u + 4]), __uint_as_float(v[8 * u + 5]), f),
+                                   epi.pack(__uint_as_float(v[8 * u + 6]), __uint_as_float(v[8 * u + 7]), f));
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -209,6 +220,21 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
 struct TcEpiTmaStore {
     static constexpr bool kStaged = true;
     int split_n = 0;
+    __device__ float factor() const { return 1.f; }
+    __device__ uint32_t pack(float lo, float hi, float) const { return pack_bf162(lo, hi); }
+    __device__ void operator()(int, int, int, const float *) const {}
+};
+
+// The same with f16 outputs scaled by 2^-e, for products of operands whose
+// largest finite magnitudes' bf16 patterns are max_bits[0] and max_bits[1]:
+// with K = 512 no product is beyond 2^9 times both, and e (half_exponent) is
+// the least that keeps that bound at 2^15.
+struct TcEpiTmaStoreHalf {
+    static constexpr bool kStaged = true;
+    const uint32_t *max_bits;
+    int split_n = 0;
+    __device__ float factor() const { return exp2_int(-half_exponent(max_bits)); }
+    __device__ uint32_t pack(float lo, float hi, float f) const { return pack_half2(lo * f, hi * f); }
     __device__ void operator()(int, int, int, const float *) const {}
 };
 

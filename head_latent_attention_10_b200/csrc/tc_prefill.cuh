@@ -29,15 +29,27 @@
 // softmax warps (2-5) find the next tile's logits ready when they finish this
 // one; warp 7 issues P(k) V_k as soon as P(k) is written.  Two issuing
 // threads, because a thread's tcgen05.mma issue blocks while the tensor pipe
-// is busy, and one thread would hold P(k+1) V back behind S(k+2).  The causal mask applies to
+// is busy, and one thread would hold P(k+1) V back behind S(k+2).  Both are chosen
+// by elect.sync: under a `lane == 0` branch the compiler takes 76 cycles to issue an
+// MMA, more than its 64 in the pipe.  The causal mask applies to
 // the tiles that straddle the diagonal; lazy rescaling as in the decode (O
 // is rescaled in TMEM only when the running max grows by more than 8, after
 // the previous P V has retired).  Every wait is bounded; no TMA load uses
 // cluster multicast.
+//
+// kHalfV: V^C and P are f16 instead of bf16 (the 4-bit cache's prefill).  The
+// latents there are read exactly, and the two roundings to 8 bits of P and V^C
+// would be two thirds of the output's error (its relative rms 0.0029 against
+// 0.0017 for the output's own rounding to bf16).  f16 needs its range kept: V^C
+// is stored times 2^-e, with e from the largest latent and weight magnitudes
+// (prefill_prepare_kernel), so that none overflows whatever the weights, and P
+// is formed as 2^7 p (p <= 2^8), which leaves weights down to 2^-21 their 11
+// bits.  Both factors are powers of two and come off in the epilogue.
 #pragma once
 
 #include "dec_common.cuh"
 #include "k_simple.cuh"
+#include "tc_gemm.cuh"
 
 namespace mla {
 
@@ -48,6 +60,7 @@ constexpr int kPfOffK = 0;                             // K slot j: chunks 3j ..
 constexpr int kPfOffV = kPfKSlots * 3 * kPfChunk;      // V slot j: 2 chunks
 constexpr int kPfOffBar = kPfOffV + kPfVSlots * 2 * kPfChunk;   // 212,992
 constexpr int kPfSmem = kPfOffBar + 256 + 1024;        // barriers, alignment slack
+constexpr float kPfHalfShift = 7.f;                    // log2 of the factor on f16 P
 constexpr uint32_t kPfTmS = 0, kPfTmO = 256, kPfTmQ = 384;   // S/P buffers at 0 and 128
 
 // Tensor maps of one call.  Rows of K^C, V^C and the gathered latents are
@@ -69,6 +82,7 @@ struct PrefillArgs {
     float scale_log2;
     float *out_lse;               // [B][s][H] or null
     uint32_t *err;
+    const uint32_t *max_bits;     // kHalfV: largest magnitudes of the latents and of U^V (bf16 patterns)
     unsigned long long limit_ns;
 };
 
@@ -83,6 +97,7 @@ __device__ __forceinline__ int prefill_tiles(int q0, int s, int L)
 
 __device__ __forceinline__ bool prefill_valid(int L, int s, int l_cap) { return L >= s && L <= l_cap; }
 
+template <bool kHalfV>
 __global__ void __launch_bounds__(kPfThreads, 1)
 tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
 {
@@ -187,9 +202,9 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
         }
     } else if (warp == 1 || warp == 7) {
         // ------------------------------------------------------ MMA issue
-        if (lane == 0) {
+        if (sm100::elect_one()) {
             const uint32_t idesc_s = sm100::idesc_bf16(128, 128, 0, 0);
-            const uint32_t idesc_o = sm100::idesc_bf16(128, 128, 0, 1);
+            const uint32_t idesc_o = kHalfV ? sm100::idesc_f16(128, 128, 0, 1) : sm100::idesc_bf16(128, 128, 0, 1);
             bool ok = nk == 0 || sm100::mbar_wait(q_ready, 0, abort_flag, a.err, lim);
             if (warp == 1) {
                 // S(k) into buffer k % 2
@@ -292,14 +307,15 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
             const float corr = rescale ? ex2(m_run - m_new) : 1.f;
             l_run *= corr;
             m_run = m_new;
-            const float mu = (m_run == -INFINITY) ? 0.f : m_run;
+            float mu = (m_run == -INFINITY) ? 0.f : m_run;
+            if (kHalfV) mu -= kPfHalfShift;
             float lsum = 0.f;
 #pragma unroll
             for (int c = 0; c < 64; ++c) {
                 const float p0 = ex2(fmaf(__uint_as_float(x[2 * c]), a.scale_log2, -mu));
                 const float p1 = ex2(fmaf(__uint_as_float(x[2 * c + 1]), a.scale_log2, -mu));
                 lsum += p0 + p1;
-                x[c] = pack_bf162(p0, p1);
+                x[c] = kHalfV ? pack_half2(p0, p1) : pack_bf162(p0, p1);
             }
             l_run += lsum;
             // P(k) over the first 64 columns of S(k), already read by this thread
@@ -334,6 +350,8 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
             sm100::tc_fence_after();
         }
         const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+        const float vf = kHalfV ? exp2_int(half_exponent(a.max_bits)) : 1.f;
+        auto o_of = [&](uint32_t x) { return kHalfV ? __uint_as_float(x) * inv * vf : __uint_as_float(x) * inv; };
         uint8_t *stage = smem + kPfOffK;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
@@ -350,15 +368,15 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
             for (int q = 0; q < 4; ++q) {
                 const int unit = ((c & 63) >> 3) + q;        // 16-byte unit of the 128-byte row
                 *reinterpret_cast<uint4 *>(chunk + r * 128 + ((unit ^ (r & 7)) << 4)) =
-                    make_uint4(pack_bf162(__uint_as_float(ov[8 * q]) * inv, __uint_as_float(ov[8 * q + 1]) * inv),
-                               pack_bf162(__uint_as_float(ov[8 * q + 2]) * inv, __uint_as_float(ov[8 * q + 3]) * inv),
-                               pack_bf162(__uint_as_float(ov[8 * q + 4]) * inv, __uint_as_float(ov[8 * q + 5]) * inv),
-                               pack_bf162(__uint_as_float(ov[8 * q + 6]) * inv, __uint_as_float(ov[8 * q + 7]) * inv));
+                    make_uint4(pack_bf162(o_of(ov[8 * q]), o_of(ov[8 * q + 1])),
+                               pack_bf162(o_of(ov[8 * q + 2]), o_of(ov[8 * q + 3])),
+                               pack_bf162(o_of(ov[8 * q + 4]), o_of(ov[8 * q + 5])),
+                               pack_bf162(o_of(ov[8 * q + 6]), o_of(ov[8 * q + 7])));
             }
         }
         if (a.out_lse && has_row)
             a.out_lse[((long long)b * a.s + t) * a.H + head] =
-                l_run > 0.f ? (m_run + __log2f(l_run)) * kLn2 : -INFINITY;
+                l_run > 0.f ? (m_run + __log2f(l_run) - (kHalfV ? kPfHalfShift : 0.f)) * kLn2 : -INFINITY;
         fence_proxy_async_smem();
         asm volatile("bar.sync 1, 128;" ::: "memory");     // the 4 softmax warps
         if (warp == 2 && lane == 0) {
@@ -380,20 +398,31 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
     }
 }
 
+// The larger of each half's finite magnitudes, as bf16 patterns, over 8 values.
+__device__ __forceinline__ uint32_t finite_max(uint4 v)
+{
+    auto fin = [](uint32_t x) { x &= 0x7FFF7FFFu; return x & __vcmpltu2(x, 0x7F807F80u); };
+    return __vmaxu2(__vmaxu2(fin(v.x), fin(v.y)), __vmaxu2(fin(v.z), fin(v.w)));
+}
+
 // Prefill set-up, one pass: each sequence's cached rows gathered through its
 // block table into rows [b * lpad, b * lpad + lpad) of a contiguous [576]-wide
 // buffer (rows at or past the sequence's length, and every row of an invalid
 // sequence, are zero), and the chunk's RoPE queries rotated to q_pos (copied
 // when q_pos is null).  Rows: how the cache's rows are read as bf16 (Bf16Rows,
-// Int4Rows).
-template <class Rows>
+// Int4Rows).  With kHalfV also the largest finite magnitudes, as bf16 patterns,
+// of the gathered latents and of the weights w_uv (w_units 16-byte units):
+// maxima, which no order of the atomics changes.
+template <class Rows, bool kHalfV>
 __global__ void __launch_bounds__(256)
 prefill_prepare_kernel(const Rows cache, int num_blocks, const int32_t *__restrict__ block_table,
                        int max_blocks, const int32_t *__restrict__ seq_lens, int B, int s, int H, int lpad,
                        int l_cap, bf16 *__restrict__ rows, const bf16 *__restrict__ q_rope,
                        const int32_t *__restrict__ q_pos, bf16 *__restrict__ q_rot, const RopeTable rope,
-                       uint32_t *err)
+                       const uint4 *__restrict__ w_uv, long long w_units, uint32_t *max_bits, uint32_t *err)
 {
+    __shared__ uint32_t cta_max[2];
+    uint32_t mc = 0, mw = 0;
     const long long tid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const long long nthreads = (long long)gridDim.x * blockDim.x;
     constexpr int kUnits = kRow / 8;                            // 16-byte units per row
@@ -414,10 +443,20 @@ prefill_prepare_kernel(const Rows cache, int num_blocks, const int32_t *__restri
                 set_error(err, MLA_DEVERR_BLOCK_ID);
         }
         reinterpret_cast<uint4 *>(rows + row * kRow)[c] = v;
+        if (kHalfV && c < kDc / 8) mc = __vmaxu2(mc, finite_max(v));
     }
     const long long units = (long long)B * s * (kDr / 2);
     for (long long w = tid; w < units; w += nthreads)
         rope_heads(q_rope, q_pos, w / (kDr / 2), (int)(w % (kDr / 2)), H, rope, q_rot, kDr, 0);
+    if constexpr (kHalfV) {
+        for (long long w = tid; w < w_units; w += nthreads) mw = __vmaxu2(mw, finite_max(w_uv[w]));
+        if (threadIdx.x < 2) cta_max[threadIdx.x] = 0;
+        __syncthreads();
+        atomicMax(&cta_max[0], max(mc & 0xFFFFu, mc >> 16));
+        atomicMax(&cta_max[1], max(mw & 0xFFFFu, mw >> 16));
+        __syncthreads();
+        if (threadIdx.x < 2) atomicMax(max_bits + threadIdx.x, cta_max[threadIdx.x]);
+    }
 }
 
 }  // namespace mla

@@ -1,7 +1,7 @@
 """GPU parity of the 4-bit latent cache: the writer and the row reader bit for
 bit against the oracle's quantizer and values, decode against a plain 64-bit
 evaluation of the formula on the rows the cache stands for, and prefill against
-the same and, bit for bit, against the bf16 prefill of those rows.
+the same and against the bf16 prefill of those rows, whose error it stays under.
 
 Decode tolerance, element by element.  With a_j the exact weights, c_j the
 cached latents and A = sum_j a_j |c_j|: the kernel rounds its weights to bf16
@@ -368,19 +368,24 @@ def run_prefill(M, cfg, d, codes, scales, max_len, rotate=True, lens=None):
 
 def plain_prefill(codes, scales, d, cfg):
     """The expanded form in 64 bits, out [B*s][H][128] and lse, with tolerances:
-    k^C, v^C, the rotated q^R, the weights and the output are rounded to bf16
-    (2^-8 relative each) and sums of 512 and 192 products are taken in fp32
-    (2^-23 relative to the sum of magnitudes each addition), so with kb, vb the
-    sums of magnitudes in k and v, a logit is off by at most dl = scale
-    (2^-8 |q||k| + (512 + 192) 2^-23 |q| kb), which moves a weight by 2 dl."""
+    k^C, the rotated q^R and the output are rounded to bf16 (2^-8 relative each),
+    v^C and the weights to f16 (2^-11 each) and sums of 512 and 192 products are
+    taken in fp32 (2^-23 relative to the sum of magnitudes each addition), so with
+    kb, vb the sums of magnitudes in k and v, a logit is off by at most dl = scale
+    (2^-8 |q||k| + (512 + 192) 2^-23 |q| kb), which moves a weight by 2 dl.  Below
+    f16's normal numbers the step is fixed: a weight times 2^7 is off by 2^-25 (the
+    row's largest is 1 or more, so 2^-32 of the sum), and a v^C times 2^-e by 2^-25,
+    where 2^(15 + e) is less than 4 times 512 times the largest latent and weight."""
     f, s, H = oracle.bf16_to_f64, cfg.s, cfg.H
     qr = oracle.rope_rows(f(d["q_rope"]).reshape(-1, 64), np.repeat(d["q_pos"], H)).reshape(cfg.T, H, 64)
     qn, wk, wv = f(d["q_nope"]), f(d["w_uk"]), f(d["w_uv"])
     out, tol = np.zeros((cfg.T, H, 128)), np.zeros((cfg.T, H, 128))
     lse, tol_lse = np.zeros((cfg.T, H)), np.zeros((cfg.T, H))
+    all_rows = [oracle.int4_values(codes[p], scales[p]).reshape(-1, 576)[:L] for p, L in
+                ((d["block_table"][b, :(L + 63) // 64], L) for b, L in enumerate(cfg.seq_lens))]
+    low = 2.0 ** -29 * max(np.abs(r[:, :512]).max() for r in all_rows) * np.abs(wv).max()
     for b, L in enumerate(cfg.seq_lens):
-        pages = d["block_table"][b, :(L + 63) // 64]
-        rows = oracle.int4_values(codes[pages], scales[pages]).reshape(-1, 576)[:L]
+        rows = all_rows[b]
         lat, key, mine = rows[:, :512], rows[:, 512:], slice(b * s, b * s + s)
         hide = np.arange(L)[None] > np.arange(L - s, L)[:, None]
         for h in range(H):
@@ -397,7 +402,8 @@ def plain_prefill(codes, scales, d, cfg):
             dl[hide] = 0
             dl = dl.max(-1)
             out[mine, h], lse[mine, h] = a @ v, m[:, 0] + np.log(e.sum(-1))
-            tol[mine, h] = ((2.0 ** -7 + 2.0 ** -14 + 2 * dl[:, None]) * (a @ np.abs(v)) + 512 * 2.0 ** -23 * (a @ vb)
+            tol[mine, h] = ((2.0 ** -10 + 2.0 ** -14 + 2 * dl[:, None]) * (a @ np.abs(v)) + 512 * 2.0 ** -23 * (a @ vb)
+                            + low + 2.0 ** -32 * np.abs(v).sum(0)
                             + 2.0 ** -8 * (1 + 2.0 ** -7) * np.abs(out[mine, h]))
             tol_lse[mine, h] = dl + 2.0 ** -16 + 2.0 ** -22 * np.abs(lse[mine, h])
     return out, lse, tol, tol_lse
@@ -406,18 +412,50 @@ def plain_prefill(codes, scales, d, cfg):
 @pytest.mark.parametrize("cfg", [C("p_one", 16, [1]), C("p_ragged", 16, [40, 300, 129], s=37, seed=40),
                                  C("p_chunk", 48, [190, 333], s=130, seed=41), C("p_128", 128, [257], s=200, seed=42)],
                          ids=lambda c: c.name)
-def test_prefill_is_the_bf16_prefill_of_the_stored_rows(M, cfg):
-    """Every stored value is a bf16 value, so the prefill over the 4-bit cache
-    has the bits of mla_prefill over those values; and it is the formula's
-    within the library's parity bar."""
+def test_prefill_is_the_formula_on_the_stored_rows(M, cfg):
+    """Element by element, and within the library's parity bar.  mla_prefill over
+    the same rows rounds v^C and the weights to bf16 as well: with many keys its
+    error is larger."""
     d = W.make_decode_inputs(cfg, with_cache_pages=False)
     codes, scales = random_cache(d, cfg.seed)
     got, lse, err, want, want_lse = run_prefill(M, cfg, d, codes, scales, max(cfg.seq_lens))
-    assert err == 0 and np.array_equal(got, want) and np.array_equal(lse, want_lse)
+    assert err == 0
     ref, rlse, tol, tol_lse = plain_prefill(codes, scales, d, cfg)
     assert np.all(np.abs(floats(got) - ref) <= tol), np.max(np.abs(floats(got) - ref) / tol)
     assert np.all(np.abs(lse - rlse) <= tol_lse), np.max(np.abs(lse - rlse) / tol_lse)
-    assert_parity(floats(got), ref, max_abs=np.inf, what=cfg.name)
+    assert np.all(np.abs(want_lse - rlse) <= tol_lse)
+    _, rel = assert_parity(floats(got), ref, max_abs=np.inf, what=cfg.name)
+    _, rel16 = assert_parity(floats(want), ref, max_abs=np.inf, what=cfg.name + " bf16")
+    assert min(cfg.seq_lens) < 40 or rel < rel16
+
+
+def test_prefill_keeps_the_range_of_its_weights(M):
+    """v^C is held in f16 under a power of two taken from the operands: weights
+    2^n times as large give 2^n times the output, to the bit, and an infinite
+    weight of one head leaves the other heads' bits alone."""
+    cfg = C("p_range", 16, [70, 200], s=33, seed=44)
+    d = W.make_decode_inputs(cfg, with_cache_pages=False)
+    codes, scales = random_cache(d, 44)
+    good, lse, err, _, _ = run_prefill(M, cfg, d, codes, scales, 200)
+    assert err == 0
+    for n in (-60, 20, 60):
+        w = oracle.bf16_to_f64(d["w_uv"]) * 2.0 ** n
+        got, lse_n, err, _, _ = run_prefill(M, cfg, dict(d, w_uv=W.f32_to_bf16_bits(w.astype(np.float32))), codes,
+                                            scales, 200)
+        assert err == 0 and np.array_equal(floats(got), floats(good) * 2.0 ** n) and np.array_equal(lse, lse_n)
+    w = d["w_uv"].copy()
+    w[3, 5, 7] = 0x7F80
+    got, _, err, _, _ = run_prefill(M, cfg, dict(d, w_uv=w), codes, scales, 200)
+    assert err == 0 and not np.isfinite(floats(got)[:, 3, 5]).any()
+    keep = np.ones((16, 128), bool)
+    keep[3, 5] = False
+    assert np.array_equal(got[:, keep], good[:, keep])
+    # the largest scale there is in every latent group
+    big = scales.copy()
+    big[..., :32] = 255
+    got, _, err, _, _ = run_prefill(M, cfg, dict(d, q_nope=np.zeros_like(d["q_nope"])), codes, big, 200)
+    ref, _, tol, _ = plain_prefill(codes, big, dict(d, q_nope=np.zeros_like(d["q_nope"])), cfg)
+    assert err == 0 and np.all(np.abs(floats(got) - ref) <= tol)
 
 
 def test_prefill_refuses_lengths_it_cannot_hold_and_skips_bad_blocks(M):
@@ -463,8 +501,9 @@ def test_a_served_sequence_end_to_end_eager_on_a_stream_and_in_a_graph(M):
     dp["block_table"] = d["block_table"]
     dp["q_pos"] = np.tile(np.arange(P), 2).astype(np.int32)
     host = lambda: (codes.cpu().numpy(), scales.cpu().numpy())  # noqa: E731
-    got, _, err, want, _ = run_prefill(M, pre, dp, *host(), P)
-    assert err == 0 and np.array_equal(got, want)
+    got, _, err, _, _ = run_prefill(M, pre, dp, *host(), P)
+    ref, _, tol, _ = plain_prefill(*host(), dp, pre)
+    assert err == 0 and np.all(np.abs(floats(got) - ref) <= tol)
     q = W.make_q_abs(cfg)
     lat = torch.empty(2, H, 512, dtype=torch.bfloat16, device="cuda")
     lse = torch.empty(2, H, dtype=torch.float32, device="cuda")
