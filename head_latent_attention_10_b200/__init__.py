@@ -119,10 +119,10 @@ def _addr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, gpu=None) -> Optional[int]:
     import torch
     if stream is None:   # the raw handle: building a Stream object costs more than the launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if gpu is None else gpu)
     return stream.cuda_stream
 
 
@@ -246,27 +246,31 @@ def mla_decode_fp8(d, q_abs, codes, scales, block_table, seq_lens, s, out_latent
         workspace.numel() * workspace.element_size(), flags, _stream(stream)), "mla_decode_fp8")
 
 
-def _tensors(where, *wanted) -> None:
-    """Raise ValueError unless every (name, tensor, dtype, shape) in `wanted` is
-    a contiguous tensor of that dtype and shape on the current GPU (whose
-    current stream the call runs on).  A tensor of None was left out by the
-    caller; the sizes given as -1 are free."""
+def _tensors(where, *wanted) -> int:
+    """The current GPU (whose current stream the call runs on), or a ValueError
+    unless every (name, tensor, dtype, shape) in `wanted` is a contiguous tensor
+    of that dtype and shape on it.  A tensor of None was left out by the caller;
+    a shape given as a number is a count of dimensions of any size."""
     import torch
-    places = {}
+    gpu = away = None   # the first tensor's place, and the name of one that is elsewhere
     for name, t, dtype, shape in wanted:
         if t is None:
             continue
-        got = t.shape
-        if t.dtype is not dtype or (got != shape and (len(got) != len(shape) or
-                                                      any(n != m and n != -1 for n, m in zip(shape, got)))):
-            want = " x ".join("any" if n == -1 else str(n) for n in shape)
-            raise ValueError(f"{where}: {name} must be {dtype} of shape {want}, got {t.dtype} of {tuple(got)}")
+        if t.dtype is not dtype or (t.dim() if type(shape) is int else t.shape) != shape:
+            want = f"{shape} dimensions" if type(shape) is int else "shape " + " x ".join(map(str, shape))
+            raise ValueError(f"{where}: {name} must be {dtype} of {want}, got {t.dtype} of {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} must be contiguous")
-        places[t.get_device()] = name
-    for place, name in places.items():
-        if place < 0 or place != torch.cuda.current_device():
-            raise ValueError(f"{where}: {name} must live on the current GPU")
+        place = t.get_device()
+        if gpu is None:
+            gpu = place
+            if place < 0 or place != torch.cuda.current_device():
+                away = name
+        elif place != gpu:
+            away = name
+    if away:
+        raise ValueError(f"{where}: {away} must live on the current GPU")
+    return gpu
 
 
 def mla_append_latent_int4(d, c_kv, k_rope, seq_idx, pos, block_table, codes, scales, err_word=None,
@@ -276,29 +280,29 @@ def mla_append_latent_int4(d, c_kv, k_rope, seq_idx, pos, block_table, codes, sc
     uint8 with a scale byte per 16 values, [num_blocks][64][36] uint8."""
     import torch
     T, nb = c_kv.shape[0], codes.shape[0]
-    _tensors("mla_append_latent_int4", ("c_kv", c_kv, torch.bfloat16, (T, 512)), ("k_rope", k_rope, torch.bfloat16, (T, 64)),
-             ("seq_idx", seq_idx, torch.int32, (T,)), ("pos", pos, torch.int32, (T,)),
-             ("block_table", block_table, torch.int32, (-1, -1)), ("codes", codes, torch.uint8, (nb, 64, 288)),
-             ("scales", scales, torch.uint8, (nb, 64, 36)), ("kv_norm_weight", kv_norm_weight, torch.bfloat16, (512,)),
-             ("err_word", err_word, torch.int32, (1,)))
+    gpu = _tensors("mla_append_latent_int4", ("c_kv", c_kv, torch.bfloat16, (T, 512)),
+                   ("k_rope", k_rope, torch.bfloat16, (T, 64)), ("seq_idx", seq_idx, torch.int32, (T,)),
+                   ("pos", pos, torch.int32, (T,)), ("block_table", block_table, torch.int32, 2),
+                   ("codes", codes, torch.uint8, (nb, 64, 288)), ("scales", scales, torch.uint8, (nb, 64, 36)),
+                   ("kv_norm_weight", kv_norm_weight, torch.bfloat16, (512,)), ("err_word", err_word, torch.int32, (1,)))
     _check(load_library().mla_append_latent_int4(
         ctypes.byref(d), c_kv.data_ptr(), k_rope.data_ptr(), T, seq_idx.data_ptr(), pos.data_ptr(),
         block_table.data_ptr(), block_table.shape[0], block_table.shape[1], codes.data_ptr(), scales.data_ptr(), nb,
-        _addr(kv_norm_weight), kv_norm_eps, _addr(err_word), _stream(stream)), "mla_append_latent_int4")
+        _addr(kv_norm_weight), kv_norm_eps, _addr(err_word), _stream(stream, gpu)), "mla_append_latent_int4")
 
 
 def mla_gather_latent_int4(d, codes, scales, seq_idx, pos, block_table, rows, err_word=None, stream=None):
     """rows[t] = the bf16 values of the 4-bit row of (seq_idx[t], pos[t])."""
     import torch
     T, nb = seq_idx.shape[0], codes.shape[0]
-    _tensors("mla_gather_latent_int4", ("seq_idx", seq_idx, torch.int32, (T,)), ("pos", pos, torch.int32, (T,)),
-             ("block_table", block_table, torch.int32, (-1, -1)), ("rows", rows, torch.bfloat16, (T, 576)),
-             ("codes", codes, torch.uint8, (nb, 64, 288)), ("scales", scales, torch.uint8, (nb, 64, 36)),
-             ("err_word", err_word, torch.int32, (1,)))
+    gpu = _tensors("mla_gather_latent_int4", ("seq_idx", seq_idx, torch.int32, (T,)), ("pos", pos, torch.int32, (T,)),
+                   ("block_table", block_table, torch.int32, 2), ("rows", rows, torch.bfloat16, (T, 576)),
+                   ("codes", codes, torch.uint8, (nb, 64, 288)), ("scales", scales, torch.uint8, (nb, 64, 36)),
+                   ("err_word", err_word, torch.int32, (1,)))
     _check(load_library().mla_gather_latent_int4(
         ctypes.byref(d), codes.data_ptr(), scales.data_ptr(), nb, seq_idx.data_ptr(), pos.data_ptr(), T,
         block_table.data_ptr(), block_table.shape[0], block_table.shape[1], rows.data_ptr(), _addr(err_word),
-        _stream(stream)), "mla_gather_latent_int4")
+        _stream(stream, gpu)), "mla_gather_latent_int4")
 
 
 def mla_decode_int4(d, q_abs, codes, scales, block_table, seq_lens, s, out_latent, out_lse, workspace,
@@ -307,14 +311,16 @@ def mla_decode_int4(d, q_abs, codes, scales, block_table, seq_lens, s, out_laten
     out_lse.  workspace: a uint8 tensor of mla_decode_workspace_size bytes."""
     import torch
     B, H, nb, mb = seq_lens.shape[0], d.num_heads, codes.shape[0], block_table.shape[-1]
-    _tensors("mla_decode_int4", ("q_abs", q_abs, torch.bfloat16, (B * s, H, 576)), ("seq_lens", seq_lens, torch.int32, (B,)),
-             ("block_table", block_table, torch.int32, (B, mb)), ("out_latent", out_latent, torch.bfloat16, (B * s, H, 512)),
-             ("out_lse", out_lse, torch.float32, (B * s, H)), ("codes", codes, torch.uint8, (nb, 64, 288)),
-             ("scales", scales, torch.uint8, (nb, 64, 36)), ("workspace", workspace, torch.uint8, (-1,)))
+    gpu = _tensors("mla_decode_int4", ("q_abs", q_abs, torch.bfloat16, (B * s, H, 576)),
+                   ("seq_lens", seq_lens, torch.int32, (B,)),
+                   ("block_table", block_table, torch.int32, (B, mb)),
+                   ("out_latent", out_latent, torch.bfloat16, (B * s, H, 512)),
+                   ("out_lse", out_lse, torch.float32, (B * s, H)), ("codes", codes, torch.uint8, (nb, 64, 288)),
+                   ("scales", scales, torch.uint8, (nb, 64, 36)), ("workspace", workspace, torch.uint8, 1))
     _check(load_library().mla_decode_int4(
         ctypes.byref(d), q_abs.data_ptr(), codes.data_ptr(), scales.data_ptr(), nb, block_table.data_ptr(), mb,
         seq_lens.data_ptr(), B, s, out_latent.data_ptr(), _addr(out_lse), workspace.data_ptr(), workspace.numel(),
-        flags, _stream(stream)), "mla_decode_int4")
+        flags, _stream(stream, gpu)), "mla_decode_int4")
 
 
 def mla_prefill_int4(d, q_nope, q_rope, q_pos, w_uk, w_uv, codes, scales, block_table, seq_lens, s, max_seq_len,
@@ -324,17 +330,17 @@ def mla_prefill_int4(d, q_nope, q_rope, q_pos, w_uk, w_uv, codes, scales, block_
     workspace: a uint8 tensor of mla_prefill_workspace_size bytes."""
     import torch
     B, H, nb, mb = seq_lens.shape[0], d.num_heads, codes.shape[0], block_table.shape[-1]
-    _tensors("mla_prefill_int4", ("q_nope", q_nope, torch.bfloat16, (B * s, H, 128)),
-             ("q_rope", q_rope, torch.bfloat16, (B * s, H, 64)), ("q_pos", q_pos, torch.int32, (B * s,)),
-             ("w_uk", w_uk, torch.bfloat16, (H, 128, 512)), ("w_uv", w_uv, torch.bfloat16, (H, 128, 512)),
-             ("block_table", block_table, torch.int32, (B, mb)), ("seq_lens", seq_lens, torch.int32, (B,)),
-             ("out", out, torch.bfloat16, (B * s, H, 128)), ("out_lse", out_lse, torch.float32, (B * s, H)),
-             ("codes", codes, torch.uint8, (nb, 64, 288)), ("scales", scales, torch.uint8, (nb, 64, 36)),
-             ("workspace", workspace, torch.uint8, (-1,)))
+    gpu = _tensors("mla_prefill_int4", ("q_nope", q_nope, torch.bfloat16, (B * s, H, 128)),
+                   ("q_rope", q_rope, torch.bfloat16, (B * s, H, 64)), ("q_pos", q_pos, torch.int32, (B * s,)),
+                   ("w_uk", w_uk, torch.bfloat16, (H, 128, 512)), ("w_uv", w_uv, torch.bfloat16, (H, 128, 512)),
+                   ("block_table", block_table, torch.int32, (B, mb)), ("seq_lens", seq_lens, torch.int32, (B,)),
+                   ("out", out, torch.bfloat16, (B * s, H, 128)), ("out_lse", out_lse, torch.float32, (B * s, H)),
+                   ("codes", codes, torch.uint8, (nb, 64, 288)), ("scales", scales, torch.uint8, (nb, 64, 36)),
+                   ("workspace", workspace, torch.uint8, 1))
     _check(load_library().mla_prefill_int4(
         ctypes.byref(d), q_nope.data_ptr(), q_rope.data_ptr(), _addr(q_pos), w_uk.data_ptr(), w_uv.data_ptr(),
         codes.data_ptr(), scales.data_ptr(), nb, block_table.data_ptr(), mb, seq_lens.data_ptr(), B, s, max_seq_len,
-        out.data_ptr(), _addr(out_lse), workspace.data_ptr(), workspace.numel(), flags, _stream(stream)),
+        out.data_ptr(), _addr(out_lse), workspace.data_ptr(), workspace.numel(), flags, _stream(stream, gpu)),
         "mla_prefill_int4")
 
 

@@ -49,24 +49,28 @@ __device__ __forceinline__ void rope_turn(float x0, float x1, int pos, double th
     *y1 = (float)((double)x0 * sn + (double)x1 * cs);
 }
 
-// RoPE pair k of every head of token tok: one angle per (token, pair), taken
-// and turned in double precision (the rotate of rope_turn), applied to the H
-// heads' rows q_rope[tok][h] (64 bf16 each) and written to dst at row
+// RoPE pair k of heads h0 .. h1 - 1 of token tok: one angle per (token, pair),
+// taken in double precision and turned in Real (the rotate of rope_turn, or in
+// fp32, whose 2^-24 the rounding to bf16 hides), applied to the heads' rows
+// q_rope[tok][h] (64 bf16 each, H of them a token) and written to dst at row
 // (tok * H + h) * dst_stride + dst_off; copied unturned when q_pos is null.
 // A warp of consecutive k covers one token's 32 pairs: coalesced per head.
+template <class Real = double>
 __device__ __forceinline__ void rope_heads(const bf16 *__restrict__ q_rope, const int32_t *__restrict__ q_pos,
                                            long long tok, int k, int H, const RopeTable &rope, bf16 *__restrict__ dst,
-                                           int dst_stride, int dst_off)
+                                           int dst_stride, int dst_off, int h0, int h1)
 {
     double sn = 0.0, cs = 1.0;
     if (q_pos) sincos((double)q_pos[tok] * rope.theta[k], &sn, &cs);
-    for (int h = 0; h < H; ++h) {
+    const Real c = (Real)cs, n = (Real)sn;
+#pragma unroll 4
+    for (int h = h0; h < h1; ++h) {
         const long long row = tok * H + h;
         const __nv_bfloat162 x = reinterpret_cast<const __nv_bfloat162 *>(q_rope + row * kDr)[k];
         __nv_bfloat162 y = x;
         if (q_pos) {
-            const double x0 = __low2float(x), x1 = __high2float(x);
-            y = __floats2bfloat162_rn((float)(x0 * cs - x1 * sn), (float)(x0 * sn + x1 * cs));
+            const Real x0 = __low2float(x), x1 = __high2float(x);
+            y = __floats2bfloat162_rn((float)(x0 * c - x1 * n), (float)(x0 * n + x1 * c));
         }
         reinterpret_cast<__nv_bfloat162 *>(dst + row * dst_stride + dst_off)[k] = y;
     }

@@ -112,7 +112,7 @@ rope_q_kernel(const bf16 *__restrict__ q_rope, const int32_t *__restrict__ q_pos
 {
     const long long units = (long long)T * (kDr / 2);
     for (long long w = (long long)blockIdx.x * blockDim.x + threadIdx.x; w < units; w += (long long)gridDim.x * blockDim.x)
-        rope_heads(q_rope, q_pos, w / (kDr / 2), (int)(w % (kDr / 2)), H, rope, dst, dst_stride, dst_off);
+        rope_heads(q_rope, q_pos, w / (kDr / 2), (int)(w % (kDr / 2)), H, rope, dst, dst_stride, dst_off, 0, H);
 }
 
 // RMS normalisation, in place, of the latent part of the cache rows of T

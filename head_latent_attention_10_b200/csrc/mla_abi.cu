@@ -8,6 +8,7 @@
 
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "absorb.cuh"
 #include "append_proj.cuh"
@@ -168,12 +169,12 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 
 // C = A B on tcgen05; `c` is the output tensor map of the staged (TMA store)
 // epilogue, unused by the others.
-template <int BN, bool kBmn, class Epi, bool kAmn = false>
+template <int BN, bool kBmn, class Epi, bool kAmn = false, int kStages = kGemmStages>
 cudaError_t launch_tc_gemm(const CUtensorMap &a, const CUtensorMap &b, int M, int N, int K, int Z, const Epi &epi,
                            uint32_t *err, cudaStream_t st, const CUtensorMap *c = nullptr)
 {
-    using S = GemmSmem<BN>;
-    auto kern = tc_gemm_kernel<BN, kBmn, Epi, kAmn>;
+    using S = GemmSmem<BN, kStages>;
+    auto kern = tc_gemm_kernel<BN, kBmn, Epi, kAmn, kStages>;
     static std::atomic<bool> attr_set[kMaxDevices];
     const cudaError_t e = ensure_smem_attr(kern, S::BYTES, attr_set);
     if (e != cudaSuccess) return e;
@@ -475,6 +476,11 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
         const uint64_t odims[4] = {(uint64_t)kDh, (uint64_t)H, (uint64_t)s, (uint64_t)B};
         const uint64_t ostr[3] = {(uint64_t)kDh * 2, (uint64_t)H * kDh * 2, (uint64_t)s * H * kDh * 2};
         const uint32_t obox[4] = {64, 1, 128, 1};
+        const uint64_t rdims[4] = {(uint64_t)kDr, (uint64_t)H, (uint64_t)s, (uint64_t)B};
+        const uint64_t rstr[3] = {(uint64_t)kDr * 2, (uint64_t)H * kDr * 2, (uint64_t)s * H * kDr * 2};
+        if (!make_tmap_4d(&pm.qn, q_nope, odims, ostr, obox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !make_tmap_4d(&pm.qr, q_rot, rdims, rstr, obox, CU_TENSOR_MAP_SWIZZLE_128B))
+            return MLA_ERR_CUDA;
         if (!make_tmap_4d(&pm.out, out, odims, ostr, obox, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !make_tmap_3d(&pm.kr, rows, kRow, M, 1, kRow * 2, (uint64_t)M * kRow * 2, 64, 128, 1,
                           CU_TENSOR_MAP_SWIZZLE_128B))
@@ -483,31 +489,27 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
         pm.vc = mvc;
     }
     if (cudaMemsetAsync(err, 0, (kHalfV ? 4 : 1) * sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
-    {
-        const long long work = rows_total * (kRow / 8) + (long long)B * s * (kDr / 2);
-        long long blocks = (work + 255) / 256;
-        if (blocks > 8ll * sm_count()) blocks = 8ll * sm_count();
-        prefill_prepare_kernel<Rows, kHalfV><<<(int)blocks, 256, 0, strm>>>(cache, num_blocks, block_table, max_blocks,
-                                                                    seq_lens, B, s, H, w.lpad, l_cap, rows,
-                                                                    (const bf16 *)q_rope, q_pos, q_rot,
-                                                                    rope_table(dims), (const uint4 *)w_uv,
-                                                                    (long long)H * kDh * kDc / 8, max_bits, err);
-        count_launch();
-        if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-    }
-    if (launch_tc_gemm<256, false, TcEpiTmaStore>(ma, muk, M, H * kDh, kDc, 1, TcEpiTmaStore{}, err, strm, &skc) !=
-        cudaSuccess)
-        return MLA_ERR_CUDA;
-    cudaError_t ve;
-    if constexpr (kHalfV)
-        ve = launch_tc_gemm<256, false, TcEpiTmaStoreHalf>(ma, muv, M, H * kDh, kDc, 1, TcEpiTmaStoreHalf{max_bits},
-                                                           err, strm, &svc);
-    else
-        ve = launch_tc_gemm<256, false, TcEpiTmaStore>(ma, muv, M, H * kDh, kDc, 1, TcEpiTmaStore{}, err, strm, &svc);
-    if (ve != cudaSuccess) return MLA_ERR_CUDA;
+    const PrepareBlocks pb(B, w.lpad, s, H, kHalfV);
+    prefill_prepare_kernel<Rows, kHalfV><<<pb.rows + pb.rope + pb.weights, 256, 0, strm>>>(
+        cache, pb, num_blocks, block_table, max_blocks, seq_lens, s, H, w.lpad, l_cap, rows, (const bf16 *)q_rope, q_pos,
+        q_rot, rope_table(dims), (const uint4 *)w_uv, max_bits, err);
+    count_launch();
+    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    // More tiles than SMs: two stages, so that two CTAs of an SM overlap one's
+    // start and epilogue with the other's products (73 us against 98 at 4,096 rows
+    // x 128 heads); fewer: four, which hide a lone CTA's loads (9.4 against 11.1 us
+    // at 1,152 rows x 16 heads).
+    auto expand = [&](const CUtensorMap &w_map, const auto &epi, const CUtensorMap &out_map) {
+        using Epi = std::decay_t<decltype(epi)>;
+        return (long long)((M + 127) / 128) * ((H * kDh + 255) / 256) > sm_count()
+            ? launch_tc_gemm<256, false, Epi, false, 2>(ma, w_map, M, H * kDh, kDc, 1, epi, err, strm, &out_map)
+            : launch_tc_gemm<256, false, Epi>(ma, w_map, M, H * kDh, kDc, 1, epi, err, strm, &out_map);
+    };
+    using VEpi = std::conditional_t<kHalfV, TcEpiTmaStoreHalf, TcEpiTmaStore>;
+    VEpi v_epi{};
+    if constexpr (kHalfV) v_epi.max_bits = max_bits;
+    if (expand(muk, TcEpiTmaStore{}, skc) != cudaSuccess || expand(muv, v_epi, svc) != cudaSuccess) return MLA_ERR_CUDA;
     PrefillArgs pa;
-    pa.q_nope = (const bf16 *)q_nope;
-    pa.q_rot = q_rot;
     pa.seq_lens = seq_lens;
     pa.s = s;
     pa.H = H;

@@ -23,12 +23,12 @@ namespace mla {
 constexpr int kGemmStages = 4;
 constexpr int kGemmThreads = 192;
 
-template <int BN>
+template <int BN, int kStages>
 struct GemmSmem {
     static constexpr int A = 128 * 64 * 2;
     static constexpr int B = BN * 64 * 2;
     static constexpr int STAGE = A + B;
-    static constexpr int BAR = kGemmStages * STAGE;
+    static constexpr int BAR = kStages * STAGE;
     static constexpr int BYTES = BAR + 256 + 1024;  // + barriers + alignment slack
     static constexpr int TMEM_COLS = BN <= 32 ? 32 : (BN <= 64 ? 64 : (BN <= 128 ? 128 : 256));
 };
@@ -43,18 +43,18 @@ __device__ __forceinline__ int half_exponent(const uint32_t *max_bits)
     return min(max(e, -126), 126);
 }
 
-template <int BN, bool kBmn, class Epi, bool kAmn = false>
+template <int BN, bool kBmn, class Epi, bool kAmn = false, int kStages = kGemmStages>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                const __grid_constant__ CUtensorMap mapC, int M, int N, int K, Epi epi, uint32_t *err,
                unsigned long long limit_ns)
 {
-    using S = GemmSmem<BN>;
+    using S = GemmSmem<BN, kStages>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::BAR);
-    uint64_t *empty = full + kGemmStages;
-    uint64_t *done = empty + kGemmStages;
+    uint64_t *empty = full + kStages;
+    uint64_t *done = empty + kStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -63,7 +63,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
     const int nk = K / 64;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kGemmStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             sm100::mbar_init(&full[s], 1);
             sm100::mbar_init(&empty[s], 1);
         }
@@ -90,8 +90,8 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
         if (sm100::elect_one()) {
             int issued = 0;
             for (int kb = 0; kb < nk; ++kb) {
-                const int s = kb % kGemmStages;
-                const uint32_t use = kb / kGemmStages;
+                const int s = kb % kStages;
+                const uint32_t use = kb / kStages;
                 if (use > 0 && !sm100::mbar_wait(&empty[s], (use - 1) & 1, abort_flag, err, limit_ns)) break;
                 issued = kb + 1;
                 uint8_t *a = smem + s * S::STAGE;
@@ -116,8 +116,8 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
                 // never leave a copy in flight into shared memory: wait for the
                 // last load issued on every stage
                 volatile int no_abort = 0;
-                for (int kb = issued - kGemmStages < 0 ? 0 : issued - kGemmStages; kb < issued; ++kb)
-                    sm100::mbar_wait(&full[kb % kGemmStages], (kb / kGemmStages) & 1, &no_abort, err, drain_ns);
+                for (int kb = issued - kStages < 0 ? 0 : issued - kStages; kb < issued; ++kb)
+                    sm100::mbar_wait(&full[kb % kStages], (kb / kStages) & 1, &no_abort, err, drain_ns);
             }
         }
     } else if (warp == 1) {
@@ -125,8 +125,8 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
             const uint32_t idesc = sm100::idesc_bf16(128, BN, kAmn ? 1 : 0, kBmn ? 1 : 0);
             bool ok = true;
             for (int kb = 0; kb < nk && ok; ++kb) {
-                const int s = kb % kGemmStages;
-                ok = sm100::mbar_wait(&full[s], (kb / kGemmStages) & 1, abort_flag, err, limit_ns);
+                const int s = kb % kStages;
+                ok = sm100::mbar_wait(&full[s], (kb / kStages) & 1, abort_flag, err, limit_ns);
                 if (!ok) break;
                 sm100::tc_fence_after();
                 const uint32_t a = sm100::smem_u32(smem + s * S::STAGE);

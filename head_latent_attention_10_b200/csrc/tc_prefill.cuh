@@ -19,7 +19,9 @@
 //   O   += P(k) V_k   N=128, K=128: 8 MMAs, P read from TMEM
 // TMEM (512 columns): S(k) in buffer k % 2 (columns 0-127, 128-255), P(k)
 // written over the first 64 columns of its S buffer, O 256-383, Q 384-479
-// (192 bf16 per row, written by the softmax warps at the start).
+// (192 bf16 per row: TMA brings the tile's queries into K slot 2, which the third
+// key tile is the first to need, and the softmax warps move them on; read from
+// global memory a row per thread they took 7,000 cycles, now 3,200).
 // With Q and P in TMEM, shared memory holds only key and value tiles: a
 // 3-slot ring of K tiles (K^C 0-63, K^C 64-127, k^R; 48 KB each) and a 2-slot
 // ring of V tiles (V^C 0-63, 64-127; 32 KB each), 208 KB, each ring fed by
@@ -47,6 +49,8 @@
 // bits.  Both factors are powers of two and come off in the epilogue.
 #pragma once
 
+#include <type_traits>
+
 #include "dec_common.cuh"
 #include "k_simple.cuh"
 #include "tc_gemm.cuh"
@@ -56,6 +60,7 @@ namespace mla {
 constexpr int kPfThreads = 256;                        // warps: 0 K loads, 1 S MMAs, 2-5 softmax, 6 V loads, 7 P V MMAs
 constexpr int kPfChunk = 128 * 128;                    // [128 rows][64 bf16], 128-byte swizzle: 16 KB
 constexpr int kPfKSlots = 3, kPfVSlots = 2;
+constexpr int kPfRopeHeads = 16;                       // heads a thread of the set-up rotates one pair of
 constexpr int kPfOffK = 0;                             // K slot j: chunks 3j .. 3j+2
 constexpr int kPfOffV = kPfKSlots * 3 * kPfChunk;      // V slot j: 2 chunks
 constexpr int kPfOffBar = kPfOffV + kPfVSlots * 2 * kPfChunk;   // 212,992
@@ -72,11 +77,11 @@ struct PrefillMaps {
     CUtensorMap vc;    // V^C   {128, H, B Lpad}, box {64, 1, 128}
     CUtensorMap kr;    // gathered rows {576, B Lpad, 1}, box {64, 128, 1}, read at x = 512
     CUtensorMap out;   // out   {128, H, s, B}, box {64, 1, 128, 1}
+    CUtensorMap qn;    // q_nope {128, H, s, B}, box {64, 1, 128, 1}
+    CUtensorMap qr;    // rotated q_rope {64, H, s, B}, box {64, 1, 128, 1}
 };
 
 struct PrefillArgs {
-    const bf16 *q_nope;           // [B*s][H][128]
-    const bf16 *q_rot;            // [B*s][H][64], rotated
     const int32_t *seq_lens;
     int s, H, lpad, l_cap;        // l_cap: the largest valid sequence length
     float scale_log2;
@@ -115,6 +120,7 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
     uint64_t *done = bars + 17;         // both issuers' last MMAs done (teardown)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 19);
+    uint64_t *q_full = bars + 20;       // Q in K slot 2
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int qb = gridDim.x - 1 - blockIdx.x;   // the longest rows of the causal triangle first
@@ -137,6 +143,7 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
             sm100::mbar_init(&pv_done[i], 1);
         }
         sm100::mbar_init(q_ready, 4);
+        sm100::mbar_init(q_full, 1);
         sm100::mbar_init(&s_full[0], 1);
         sm100::mbar_init(&s_full[1], 1);
         sm100::mbar_init(done, 2);
@@ -145,6 +152,8 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
         sm100::prefetch_tensormap(&maps.kc);
         sm100::prefetch_tensormap(&maps.vc);
         sm100::prefetch_tensormap(&maps.kr);
+        sm100::prefetch_tensormap(&maps.qn);
+        sm100::prefetch_tensormap(&maps.qr);
     }
     if (warp == 1) {
         sm100::tmem_alloc(tmem_slot, 512);
@@ -161,8 +170,14 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
         // ----------------------------------------------------------- K loads
         if (lane == 0 && nk > 0) {
             int issued = 0;
+            uint8_t *qs = smem + kPfOffK + 3 * (kPfKSlots - 1) * kPfChunk;
+            sm100::mbar_arrive_expect_tx(q_full, 3 * kPfChunk);
+            sm100::tma_load_4d(&maps.qn, q_full, qs, 0, head, q0, b);
+            sm100::tma_load_4d(&maps.qn, q_full, qs + kPfChunk, 64, head, q0, b);
+            sm100::tma_load_4d(&maps.qr, q_full, qs + 2 * kPfChunk, 0, head, q0, b);
             for (int k = 0; k < nk; ++k) {
                 const int sl = k % kPfKSlots;
+                if (k == kPfKSlots - 1 && !sm100::mbar_wait(q_ready, 0, abort_flag, a.err, lim)) break;
                 if (k >= kPfKSlots &&
                     !sm100::mbar_wait(&k_free[sl], ((k / kPfKSlots) - 1) & 1, abort_flag, a.err, lim))
                     break;
@@ -176,6 +191,7 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
             }
             if (*abort_flag) {   // let the copies in flight land before the CTA can exit
                 volatile int no_abort = 0;
+                sm100::mbar_wait(q_full, 0, &no_abort, a.err, drain);
                 for (int k = issued - kPfKSlots < 0 ? 0 : issued - kPfKSlots; k < issued; ++k)
                     sm100::mbar_wait(&k_full[k % kPfKSlots], (k / kPfKSlots) & 1, &no_abort, a.err, drain);
             }
@@ -260,18 +276,15 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
         const int nvis = has_row ? L - a.s + t + 1 : 0;   // keys [0, nvis) visible to row t
         bool ok = true;
         if (nk > 0) {
-            // this row's query [q^C | rotated q^R] into TMEM (192 bf16 = 96 columns)
-            const long long qrow = ((long long)b * a.s + (has_row ? t : 0)) * a.H + head;
-            const uint4 *qc = reinterpret_cast<const uint4 *>(a.q_nope + qrow * kDh);
-            const uint4 *qr = reinterpret_cast<const uint4 *>(a.q_rot + qrow * kDr);
+            // this row's query [q^C | rotated q^R] into TMEM (192 bf16 = 96 columns;
+            // rows past the sequence's queries arrive as zeros)
+            ok = sm100::warp_wait(q_full, 0, abort_flag, a.err, lim);
+            const uint32_t qs = sm100::smem_u32(smem + kPfOffK + 3 * (kPfKSlots - 1) * kPfChunk) + r * 128;
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
                 uint4 v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int u = 8 * c + e;   // 16-byte unit of the 384-byte row
-                    v[e] = !has_row ? make_uint4(0, 0, 0, 0) : (u < 16 ? __ldg(qc + u) : __ldg(qr + (u - 16)));
-                }
+                for (int e = 0; e < 8; ++e) v[e] = ld_shared_v4(qs + c * kPfChunk + ((e ^ (r & 7)) << 4));
                 sm100::tmem_st32(tm_q + 32 * c, reinterpret_cast<const uint32_t *>(v));
             }
             sm100::tmem_wait_st();
@@ -405,57 +418,86 @@ __device__ __forceinline__ uint32_t finite_max(uint4 v)
     return __vmaxu2(__vmaxu2(fin(v.x), fin(v.y)), __vmaxu2(fin(v.z), fin(v.w)));
 }
 
-// Prefill set-up, one pass: each sequence's cached rows gathered through its
-// block table into rows [b * lpad, b * lpad + lpad) of a contiguous [576]-wide
-// buffer (rows at or past the sequence's length, and every row of an invalid
-// sequence, are zero), and the chunk's RoPE queries rotated to q_pos (copied
-// when q_pos is null).  Rows: how the cache's rows are read as bf16 (Bf16Rows,
-// Int4Rows).  With kHalfV also the largest finite magnitudes, as bf16 patterns,
-// of the gathered latents and of the weights w_uv (w_units 16-byte units):
-// maxima, which no order of the atomics changes.
+// Prefill set-up, one launch of three kinds of CTAs (PrepareBlocks):
+//   - each sequence's cached rows gathered through its block table into rows
+//     [b * lpad, b * lpad + lpad) of a contiguous [576]-wide buffer (rows at or past
+//     the sequence's length, and every row of an invalid sequence, are zero);
+//   - the chunk's RoPE queries rotated to q_pos (copied when q_pos is null), a
+//     warp taking one token's 32 pairs of up to 16 heads;
+//   - kHalfV: the largest finite magnitudes, as bf16 patterns, of the gathered
+//     latents and of the weights w_uv (maxima, which no order of the atomics
+//     changes).
+// Every thread has one piece of work: phases one after the other in each thread
+// left the memory waiting for the angles.  Rows: how the cache's rows are read as
+// bf16 (Bf16Rows, Int4Rows).
+struct PrepareBlocks {
+    long long row_units, rope_units, w_units;   // 16-byte units; (token, heads, pair); 16-byte units
+    unsigned rows, rope, weights;               // CTAs
+    PrepareBlocks(int B, int lpad, int s, int H, bool half_v)
+        : row_units((long long)B * lpad * (kRow / 8)),
+          rope_units((long long)B * s * ((H + kPfRopeHeads - 1) / kPfRopeHeads) * (kDr / 2)),
+          w_units(half_v ? (long long)H * kDh * kDc / 8 : 0), rows((unsigned)((row_units + 255) / 256)),
+          rope((unsigned)((rope_units + 255) / 256)), weights((unsigned)((w_units + 1023) / 1024))
+    {
+    }
+};
+
 template <class Rows, bool kHalfV>
 __global__ void __launch_bounds__(256)
-prefill_prepare_kernel(const Rows cache, int num_blocks, const int32_t *__restrict__ block_table,
-                       int max_blocks, const int32_t *__restrict__ seq_lens, int B, int s, int H, int lpad,
-                       int l_cap, bf16 *__restrict__ rows, const bf16 *__restrict__ q_rope,
+prefill_prepare_kernel(const Rows cache, const PrepareBlocks blocks, int num_blocks,
+                       const int32_t *__restrict__ block_table, int max_blocks, const int32_t *__restrict__ seq_lens,
+                       int s, int H, int lpad, int l_cap, bf16 *__restrict__ rows, const bf16 *__restrict__ q_rope,
                        const int32_t *__restrict__ q_pos, bf16 *__restrict__ q_rot, const RopeTable rope,
-                       const uint4 *__restrict__ w_uv, long long w_units, uint32_t *max_bits, uint32_t *err)
+                       const uint4 *__restrict__ w_uv, uint32_t *max_bits, uint32_t *err)
 {
-    __shared__ uint32_t cta_max[2];
-    uint32_t mc = 0, mw = 0;
-    const long long tid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const long long nthreads = (long long)gridDim.x * blockDim.x;
-    constexpr int kUnits = kRow / 8;                            // 16-byte units per row
-    const long long row_units = (long long)B * lpad * kUnits;
-    for (long long w = tid; w < row_units; w += nthreads) {
-        const long long row = w / kUnits;
-        const int c = (int)(w % kUnits);
-        const int b = (int)(row / lpad), j = (int)(row % lpad);
-        const int L = seq_lens[b];
-        const bool valid = prefill_valid(L, s, l_cap);
-        if (!valid && j == 0 && c == 0) set_error(err, MLA_DEVERR_SEQ_LEN);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (valid && j < L) {
-            const int blk = block_table[(long long)b * max_blocks + j / kBlock];
-            if (blk >= 0 && blk < num_blocks)
-                v = cache.unit((long long)blk * kBlock + j % kBlock, c);
-            else if (c == 0)
-                set_error(err, MLA_DEVERR_BLOCK_ID);
+    unsigned cta = blockIdx.x;
+    uint32_t most = 0;   // kHalfV: bf16 patterns of magnitudes, a pair
+    const bool weights = cta >= blocks.rows + blocks.rope;
+    if (cta < blocks.rows) {
+        constexpr int kUnits = kRow / 8;                            // 16-byte units per row
+        const long long w = cta * 256ll + threadIdx.x;
+        if (w < blocks.row_units) {
+            const unsigned row = (unsigned)(w / kUnits);
+            const int c = (int)(w % kUnits);
+            const int b = (int)(row / lpad), j = (int)(row % lpad);
+            const int L = seq_lens[b];
+            const bool valid = prefill_valid(L, s, l_cap);
+            if (!valid && j == 0 && c == 0) set_error(err, MLA_DEVERR_SEQ_LEN);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (valid && j < L) {
+                const int blk = block_table[(long long)b * max_blocks + j / kBlock];
+                if (blk >= 0 && blk < num_blocks)
+                    v = cache.unit((long long)blk * kBlock + j % kBlock, c);
+                else if (c == 0)
+                    set_error(err, MLA_DEVERR_BLOCK_ID);
+            }
+            reinterpret_cast<uint4 *>(rows + (long long)row * kRow)[c] = v;
+            if (kHalfV && c < kDc / 8) most = finite_max(v);
         }
-        reinterpret_cast<uint4 *>(rows + row * kRow)[c] = v;
-        if (kHalfV && c < kDc / 8) mc = __vmaxu2(mc, finite_max(v));
+    } else if (!weights) {
+        const unsigned hgroups = (H + kPfRopeHeads - 1) / kPfRopeHeads;
+        const long long w = (cta - blocks.rows) * 256ll + threadIdx.x;
+        if (w < blocks.rope_units) {
+            const unsigned g = (unsigned)(w / (kDr / 2));
+            const int h0 = (int)(g % hgroups) * kPfRopeHeads;
+            rope_heads<std::conditional_t<kHalfV, float, double>>(q_rope, q_pos, g / hgroups, (int)(w % (kDr / 2)), H, rope,
+                                                                  q_rot, kDr, 0, h0, min(H, h0 + kPfRopeHeads));
+        }
+        return;
+    } else {
+        const long long w = (cta - blocks.rows - blocks.rope) * 1024ll + threadIdx.x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (w + 256 * e < blocks.w_units) most = __vmaxu2(most, finite_max(w_uv[w + 256 * e]));
     }
-    const long long units = (long long)B * s * (kDr / 2);
-    for (long long w = tid; w < units; w += nthreads)
-        rope_heads(q_rope, q_pos, w / (kDr / 2), (int)(w % (kDr / 2)), H, rope, q_rot, kDr, 0);
     if constexpr (kHalfV) {
-        for (long long w = tid; w < w_units; w += nthreads) mw = __vmaxu2(mw, finite_max(w_uv[w]));
-        if (threadIdx.x < 2) cta_max[threadIdx.x] = 0;
+        __shared__ uint32_t cta_max;
+        if (threadIdx.x == 0) cta_max = 0;
         __syncthreads();
-        atomicMax(&cta_max[0], max(mc & 0xFFFFu, mc >> 16));
-        atomicMax(&cta_max[1], max(mw & 0xFFFFu, mw >> 16));
+        most = __reduce_max_sync(0xffffffffu, max(most & 0xFFFFu, most >> 16));
+        if ((threadIdx.x & 31) == 0) atomicMax(&cta_max, most);
         __syncthreads();
-        if (threadIdx.x < 2) atomicMax(max_bits + threadIdx.x, cta_max[threadIdx.x]);
+        if (threadIdx.x == 0) atomicMax(max_bits + (weights ? 1 : 0), cta_max);
     }
 }
 
