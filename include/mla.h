@@ -378,8 +378,8 @@ mla_status_t mla_decode_fp8(const mla_dims_t *dims, const void *q_abs, const voi
  * same bf16 row (copy or RMSNorm of c_kv, RoPE of k_rope at pos) and writes
  * its codes and scales to the slot of (seq_idx[t], pos[t]): s is the
  * group's amax * (1/7), both in fp32, rounded to nearest-even at three mantissa
- * bits and clamped to the range above; u = 8 + x / s (fp32), rounded to nearest-even, u - 8
- * clamped to [-7, 7].  A NaN is stored as 0, an infinity as the largest value
+ * bits and clamped to the range above; u = 8 + x / s, rounded to nearest-even,
+ * u - 8 clamped to [-7, 7].  A NaN is stored as 0, an infinity as the largest value
  * of the largest scale.  Arguments as for mla_append_latent, with `codes` and
  * `scales` in place of `cache` (num_blocks pages of each).  T is at most 2^26
  * (MLA_ERR_UNSUPPORTED).  The tokens' slots must differ: of two tokens with
@@ -424,10 +424,11 @@ mla_status_t mla_decode_int4(const mla_dims_t *dims, const void *q_abs, const vo
 /*
  * mla_prefill_int4 -- mla_prefill over the 4-bit cache: the same attention on
  * the rows the cache stands for (the chunk's own rows included: append them
- * first).  Arguments, workspace
- * (mla_prefill_workspace_size), outputs and errors as for mla_prefill, with
- * `codes` and `scales` in place of `cache`; at most 65,535 sequences, and the
- * size limits of mla_decode_int4 (MLA_ERR_UNSUPPORTED).
+ * first).  Arguments, workspace (mla_prefill_workspace_size), outputs and errors
+ * as for mla_prefill, with `codes` and `scales` in place of `cache`; at most
+ * 65,535 sequences, and the size limits of mla_decode_int4
+ * (MLA_ERR_UNSUPPORTED).  v^C and the softmax weights are rounded to f16 (under a
+ * power of two that keeps v^C in range) where mla_prefill rounds them to bf16.
  */
 mla_status_t mla_prefill_int4(const mla_dims_t *dims, const void *q_nope, const void *q_rope,
                               const int32_t *q_pos, const void *w_uk, const void *w_uv,

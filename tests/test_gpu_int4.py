@@ -315,6 +315,25 @@ def test_writer_on_unusual_values(M):
     assert err == 0 and np.array_equal(codes[:, 0], want_c) and np.array_equal(scales[:, 0], want_s)
 
 
+@pytest.mark.parametrize("exp", [-12, 0, 18], ids=["low", "middle", "high"])
+def test_writer_rounds_every_quotient(M, exp):
+    """For a group's largest value at each of the 128 bf16 mantissas (exponents in
+    the scale's range, and where it ends), every bf16 value from 2^-7 of it up, in
+    both signs: the oracle's codes, ties among them."""
+    top = np.arange(128, dtype=np.int64) + ((127 + exp) << 7)              # bf16 patterns
+    below = np.array([np.arange(t - 7 * 128, t + 1) for t in top])         # 128 x 897
+    sign = (np.arange(below.size).reshape(below.shape) % 2) << 15
+    vals = np.concatenate([below | sign, np.zeros((128, 3), np.int64)], axis=1).reshape(128, 60, 15)
+    groups = np.concatenate([np.broadcast_to(top[:, None, None], (128, 60, 1)), vals], axis=2).reshape(-1, 32, 16)
+    T = groups.shape[0]
+    latent, key = groups.reshape(T, 512).astype(np.uint16), np.zeros((T, 64), np.uint16)
+    table = np.arange((T + 63) // 64, dtype=np.int32)[None]
+    codes, scales, err = append(M, M.dims(16), latent, key, np.zeros(T), np.arange(T), table, table.size)
+    want_c, want_s = oracle.int4_quantize_rows(W.bf16_bits_to_f32(np.concatenate([latent, key], axis=1)))
+    assert err == 0 and np.array_equal(codes.reshape(-1, 288)[:T], want_c)
+    assert np.array_equal(scales.reshape(-1, 36)[:T], want_s)
+
+
 def test_writer_and_reader_report_bad_places(M):
     import torch
     rng = np.random.default_rng(6)
@@ -573,3 +592,41 @@ def test_two_decodes_at_once_on_two_streams(M):
     torch.cuda.synchronize()
     for r, w in zip(runs, want):
         assert np.array_equal(host_bits(r[7]), w)
+
+
+def test_prefill_in_a_graph_and_on_two_streams(M):
+    """A captured call takes its operands' range anew at each replay, and two calls
+    with workspaces of their own may overlap: the eager calls' bits."""
+    import torch
+    runs, want = [], []
+    for H, lens, q, seed in ((128, [300, 140], 140, 70), (16, [1000, 257, 64], 64, 71)):
+        cfg = C("pf", H, lens, s=q, seed=seed)
+        d = W.make_decode_inputs(cfg, with_cache_pages=False)
+        codes, scales = random_cache(d, seed)
+        dims, most = M.dims(H), max(lens)
+        want.append(run_prefill(M, cfg, d, codes, scales, most)[0])
+        ws = torch.empty(M.mla_prefill_workspace_size(dims, cfg.B, q, most), dtype=torch.uint8, device="cuda")
+        out = torch.empty(cfg.T, H, 128, dtype=torch.bfloat16, device="cuda")
+        w_uv = torch_bits(d["w_uv"])
+        runs.append((dims, torch_bits(d["q_nope"]), torch_bits(d["q_rope"]), i32(d["q_pos"]), torch_bits(d["w_uk"]), w_uv,
+                     dev(codes), dev(scales), dev(d["block_table"]), dev(d["seq_lens"]), q, most, out, None, ws))
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, r in zip(streams, runs):
+            with torch.cuda.stream(st):
+                M.mla_prefill_int4(*r)
+    torch.cuda.synchronize()
+    for r, w in zip(runs, want):
+        assert np.array_equal(host_bits(r[12]), w)
+    r, graph = runs[0], torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.mla_prefill_int4(*r)
+    for n in (0, 30, -30, 0):
+        scale = 2.0 ** n
+        r[5].mul_(scale)
+        r[12].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(floats(host_bits(r[12])), floats(want[0]) * scale)
+        r[5].mul_(1 / scale)
