@@ -481,14 +481,15 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
         if (!make_tmap_4d(&pm.qn, q_nope, odims, ostr, obox, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !make_tmap_4d(&pm.qr, q_rot, rdims, rstr, obox, CU_TENSOR_MAP_SWIZZLE_128B))
             return MLA_ERR_CUDA;
-        if (!make_tmap_4d(&pm.out, out, odims, ostr, obox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        const uint32_t wbox[4] = {64, 1, 32, 1};
+        if (!make_tmap_4d(&pm.out, out, odims, ostr, wbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !make_tmap_3d(&pm.kr, rows, kRow, M, 1, kRow * 2, (uint64_t)M * kRow * 2, 64, 128, 1,
                           CU_TENSOR_MAP_SWIZZLE_128B))
             return MLA_ERR_CUDA;
         pm.kc = mkc;
         pm.vc = mvc;
     }
-    if (cudaMemsetAsync(err, 0, (kHalfV ? 4 : 1) * sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
+    if (cudaMemsetAsync(err, 0, 8 * sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
     const PrepareBlocks pb(B, w.lpad, s, H, kHalfV);
     prefill_prepare_kernel<Rows, kHalfV><<<pb.rows + pb.rope + pb.weights, 256, 0, strm>>>(
         cache, pb, num_blocks, block_table, max_blocks, seq_lens, s, H, w.lpad, l_cap, rows, (const bf16 *)q_rope, q_pos,
@@ -519,10 +520,15 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
     pa.out_lse = out_lse;
     pa.err = err;
     pa.max_bits = max_bits;
+    pa.counter = (int *)(err + 4);
+    pa.qtiles = (s + 127) / 128;
+    pa.items = pa.qtiles * H * B;
     pa.limit_ns = kWaitLimitNs;
     static std::atomic<bool> attr_set[kMaxDevices];
     if (ensure_smem_attr(tc_prefill_kernel<kHalfV>, kPfSmem, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
-    tc_prefill_kernel<kHalfV><<<dim3((s + 127) / 128, H, B), kPfThreads, kPfSmem, strm>>>(pm, pa);
+    const int ctas = sm_count();
+    if (ctas <= 0) return MLA_ERR_CUDA;
+    tc_prefill_kernel<kHalfV><<<pa.items < ctas ? pa.items : ctas, kPfThreads, kPfSmem, strm>>>(pm, pa);
     count_launch();
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
     if (flags & MLA_SYNC_CHECK) {

@@ -12,32 +12,44 @@
 // With many queries per sequence the expanded form costs fewer flops than the
 // absorbed one (2 (192 + 128) per query, key and head against 2 (576 + 512)),
 // and the step is bound by the tensor cores: a FlashAttention-style loop on
-// tcgen05.  CTA (128-query tile, head i, sequence b), the tile as MMA M = 128,
-// streams 128-key tiles of K = [K^C | k^R] and V^C:
+// tcgen05.  An item is (128-query tile, head i, sequence b), the tile as MMA
+// M = 128; it streams 128-key tiles of K = [K^C | k^R] and V^C:
 //   S(k) = Q K_k^T    N=128, K=192: 12 MMAs, Q read from TMEM
-//   P(k) = exp2(S(k) scale log2 e - m)           bf16, one thread per query row
+//   P(k) = exp2(S(k) scale log2 e - m)           one thread per query row
 //   O   += P(k) V_k   N=128, K=128: 8 MMAs, P read from TMEM
-// TMEM (512 columns): S(k) in buffer k % 2 (columns 0-127, 128-255), P(k)
-// written over the first 64 columns of its S buffer, O 256-383, Q 384-479
-// (192 bf16 per row: TMA brings the tile's queries into K slot 2, which the third
-// key tile is the first to need, and the softmax warps move them on; read from
-// global memory a row per thread they took 7,000 cycles, now 3,200).
-// With Q and P in TMEM, shared memory holds only key and value tiles: a
-// 3-slot ring of K tiles (K^C 0-63, K^C 64-127, k^R; 48 KB each) and a 2-slot
-// ring of V tiles (V^C 0-63, 64-127; 32 KB each), 208 KB, each ring fed by
-// its own loader warp (0: K, 6: V) so that neither waits behind the other.
-// Warp 1 keeps the logits one tile ahead: S(0), S(1), then S(k+2) into
-// buffer k % 2 once P(k) V_k has completed (S(k+2) overwrites P(k)), so the
-// softmax warps (2-5) find the next tile's logits ready when they finish this
-// one; warp 7 issues P(k) V_k as soon as P(k) is written.  Two issuing
-// threads, because a thread's tcgen05.mma issue blocks while the tensor pipe
-// is busy, and one thread would hold P(k+1) V back behind S(k+2).  Both are chosen
-// by elect.sync: under a `lane == 0` branch the compiler takes 76 cycles to issue an
-// MMA, more than its 64 in the pipe.  The causal mask applies to
-// the tiles that straddle the diagonal; lazy rescaling as in the decode (O
+// One CTA an SM takes items until none is left (the first by its index, more from a
+// counter; within a head the longest rows first, so a head's K and V stay in L2).
+// A CTA per item started each with 8,400 idle cycles (queries 3,200, the first
+// logits 2,000, output 2,600, set-up 600) beside 2,050 a key tile; here the next
+// item's queries and tiles are loaded ahead, and its first logits are formed while
+// the last item's output is written (916 against 995 us for a call of 4,096 tokens
+// x 128 heads).
+// TMEM (512 columns): S(t) of the CTA's tile t in buffer t % 2 (columns 0-127,
+// 128-255), P(t) written over the first 64 columns of its S buffer, O 256-383, Q
+// 384-479 (192 bf16 per row).  With Q and P in TMEM, shared memory holds a 3-slot
+// ring of K tiles (K^C 0-63, K^C 64-127, k^R; 48 KB each), in which an item's
+// queries, of the same size, take the slot before its first tile until the softmax
+// warps have moved them on (read from global memory, a row per thread, they took
+// 7,000 cycles), and a 2-slot ring of V tiles (V^C 0-63, 64-127; 32 KB each), 208 KB,
+// each ring fed by its own loader warp (0: K, 6: V) so that neither waits behind the
+// other.
+// Warp 1 keeps the logits one tile ahead: S(t+2) goes into buffer t % 2 once P(t) V
+// has completed (S(t+2) overwrites P(t)), so the softmax warps (2-5) find the next
+// tile's logits ready when they finish this one; warp 7 issues P(t) V as soon as
+// P(t) is written.  Two issuing threads, because a thread's tcgen05.mma issue blocks
+// while the tensor pipe is busy, and one thread would hold P(t+1) V back behind
+// S(t+2).  Both are chosen by elect.sync: under a `lane == 0` branch the compiler
+// takes 76 cycles to issue an MMA, more than its 64 in the pipe.  The causal mask
+// applies to the tiles that straddle the diagonal; lazy rescaling as in the decode (O
 // is rescaled in TMEM only when the running max grows by more than 8, after
 // the previous P V has retired).  Every wait is bounded; no TMA load uses
 // cluster multicast.
+//
+// What bounds a tile: two chains of about 2,000 cycles that take turns.  The softmax
+// takes 1,500 a tile (its 128 exponentials a thread 1,024 of them in their pipe); P V
+// and the S behind it 1,280 in the tensor pipe and about 600 of waits.  Eight softmax
+// warps, two threads to a row, took as long (the exponentials' pipe is the same, and
+// the two must exchange maxima).
 //
 // kHalfV: V^C and P are f16 instead of bf16 (the 4-bit cache's prefill).  The
 // latents there are read exactly, and the two roundings to 8 bits of P and V^C
@@ -63,8 +75,11 @@ constexpr int kPfKSlots = 3, kPfVSlots = 2;
 constexpr int kPfRopeHeads = 16;                       // heads a thread of the set-up rotates one pair of
 constexpr int kPfOffK = 0;                             // K slot j: chunks 3j .. 3j+2
 constexpr int kPfOffV = kPfKSlots * 3 * kPfChunk;      // V slot j: 2 chunks
-constexpr int kPfOffBar = kPfOffV + kPfVSlots * 2 * kPfChunk;   // 212,992
-constexpr int kPfSmem = kPfOffBar + 256 + 1024;        // barriers, alignment slack
+constexpr int kPfOffOut = kPfOffV + kPfVSlots * 2 * kPfChunk;   // 212,992: 32 output rows x 128 B of a softmax warp
+constexpr int kPfOffBar = kPfOffOut + 4 * 32 * 128;
+constexpr int kPfSmem = kPfOffBar + 384 + 1024;        // barriers and the item list, alignment slack
+constexpr int kPfList = 8;                             // published items
+constexpr int kPfReaders = 7;                          // S, V and P V warps, four softmax warps
 constexpr float kPfHalfShift = 7.f;                    // log2 of the factor on f16 P
 constexpr uint32_t kPfTmS = 0, kPfTmO = 256, kPfTmQ = 384;   // S/P buffers at 0 and 128
 
@@ -76,14 +91,16 @@ struct PrefillMaps {
     CUtensorMap kc;    // K^C   {128, H, B Lpad}, box {64, 1, 128}
     CUtensorMap vc;    // V^C   {128, H, B Lpad}, box {64, 1, 128}
     CUtensorMap kr;    // gathered rows {576, B Lpad, 1}, box {64, 128, 1}, read at x = 512
-    CUtensorMap out;   // out   {128, H, s, B}, box {64, 1, 128, 1}
+    CUtensorMap out;   // out   {128, H, s, B}, box {64, 1, 32, 1}
     CUtensorMap qn;    // q_nope {128, H, s, B}, box {64, 1, 128, 1}
     CUtensorMap qr;    // rotated q_rope {64, H, s, B}, box {64, 1, 128, 1}
 };
 
 struct PrefillArgs {
     const int32_t *seq_lens;
+    int *counter;                 // items taken beyond the first of each CTA (zeroed)
     int s, H, lpad, l_cap;        // l_cap: the largest valid sequence length
+    int qtiles, items;            // 128-query tiles of a sequence; times heads and sequences
     float scale_log2;
     float *out_lse;               // [B][s][H] or null
     uint32_t *err;
@@ -109,8 +126,8 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
     extern __shared__ uint8_t pf_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(pf_smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kPfOffBar);
-    uint64_t *k_full = bars;            // [3] K slot loaded
-    uint64_t *k_free = bars + 3;        // [3] S of the slot's tile done
+    uint64_t *k_full = bars;            // [3] K slot loaded (a key tile, or an item's queries)
+    uint64_t *k_free = bars + 3;        // [3] S of the slot's tile done, or the queries in TMEM
     uint64_t *v_full = bars + 6;        // [2] V slot loaded
     uint64_t *v_free = bars + 8;        // [2] P V of the slot's tile done
     uint64_t *q_ready = bars + 10;      // Q in TMEM (4 softmax warps)
@@ -120,17 +137,11 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
     uint64_t *done = bars + 17;         // both issuers' last MMAs done (teardown)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 19);
-    uint64_t *q_full = bars + 20;       // Q in K slot 2
+    volatile int *listed = reinterpret_cast<volatile int *>(bars + 20);   // items published
+    volatile int *list = reinterpret_cast<volatile int *>(bars + 21);     // [kPfList]
+    volatile int *read_to = list + kPfList;                               // [kPfReaders] items each has read
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int qb = gridDim.x - 1 - blockIdx.x;   // the longest rows of the causal triangle first
-    const int head = blockIdx.y, b = blockIdx.z;
-    const int q0 = 128 * qb;
-    const int L = a.seq_lens[b];
-    const bool valid = prefill_valid(L, a.s, a.l_cap);
-    const int nk = valid ? prefill_tiles(q0, a.s, L) : 0;
-    const int row0 = b * a.lpad;                 // this sequence's first key row
-
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPfKSlots; ++i) {
             sm100::mbar_init(&k_full[i], 1);
@@ -143,11 +154,11 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
             sm100::mbar_init(&pv_done[i], 1);
         }
         sm100::mbar_init(q_ready, 4);
-        sm100::mbar_init(q_full, 1);
         sm100::mbar_init(&s_full[0], 1);
         sm100::mbar_init(&s_full[1], 1);
         sm100::mbar_init(done, 2);
-        *abort_flag = 0;
+        *abort_flag = *listed = 0;
+        for (int i = 0; i < kPfReaders; ++i) read_to[i] = 0;
         sm100::fence_mbar_init();
         sm100::prefetch_tensormap(&maps.kc);
         sm100::prefetch_tensormap(&maps.vc);
@@ -166,89 +177,160 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
     const unsigned long long lim = a.limit_ns;
     const unsigned long long drain = lim > 200000000ull ? lim : 200000000ull;
 
+    // An item: 128 queries of one head of one sequence; within a head the longest rows
+    // of the causal triangle first.
+    struct Item {
+        int head, b, q0, L, nk;   // nk: key tiles, 0 if the sequence is invalid; -1: no more items
+    };
+    auto item_of = [&](int n) -> Item {
+        if (n >= a.items) return {0, 0, 0, 0, -1};
+        const int hb = n / a.qtiles, q0 = 128 * (a.qtiles - 1 - (n - hb * a.qtiles)), b = hb / a.H;
+        const int L = a.seq_lens[b];
+        return {hb - b * a.H, b, q0, L, prefill_valid(L, a.s, a.l_cap) ? prefill_tiles(q0, a.s, L) : 0};
+    };
+    // bounded wait of one thread for a count in shared memory
+    auto count_wait = [&](volatile int *cnt, int target) -> bool {
+        unsigned long long t0 = 0;
+        for (uint32_t i = 1; *cnt < target; ++i) {
+            if (i & 255u) continue;
+            const unsigned long long now = sm100::globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (*abort_flag) return false;
+            if (now - t0 > lim) {
+                set_error(a.err, MLA_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+                return false;
+            }
+        }
+        return true;
+    };
+    // the CTA's item j, for reader `who`, by one thread
+    auto item_at = [&](int j, int who, Item &it) -> bool {
+        if (!count_wait(listed, j + 1)) return false;
+        it = item_of(list[j % kPfList]);
+        __threadfence_block();
+        read_to[who] = j + 1;
+        return true;
+    };
+
     if (warp == 0) {
-        // ----------------------------------------------------------- K loads
-        if (lane == 0 && nk > 0) {
-            int issued = 0;
-            uint8_t *qs = smem + kPfOffK + 3 * (kPfKSlots - 1) * kPfChunk;
-            sm100::mbar_arrive_expect_tx(q_full, 3 * kPfChunk);
-            sm100::tma_load_4d(&maps.qn, q_full, qs, 0, head, q0, b);
-            sm100::tma_load_4d(&maps.qn, q_full, qs + kPfChunk, 64, head, q0, b);
-            sm100::tma_load_4d(&maps.qr, q_full, qs + 2 * kPfChunk, 0, head, q0, b);
-            for (int k = 0; k < nk; ++k) {
-                const int sl = k % kPfKSlots;
-                if (k == kPfKSlots - 1 && !sm100::mbar_wait(q_ready, 0, abort_flag, a.err, lim)) break;
-                if (k >= kPfKSlots &&
-                    !sm100::mbar_wait(&k_free[sl], ((k / kPfKSlots) - 1) & 1, abort_flag, a.err, lim))
-                    break;
-                uint8_t *dst = smem + kPfOffK + 3 * sl * kPfChunk;
-                const int r = row0 + 128 * k;
+        // ------------------------------------ items, queries and K loads
+        if (lane == 0) {
+            int issued = 0;   // ring entries: an item's queries, then its key tiles
+            auto publish = [&](int j, int n) -> bool {
+                for (int i = 0; j >= kPfList && i < kPfReaders; ++i)   // the entry it replaces is read
+                    if (!count_wait(&read_to[i], j - kPfList + 1)) return false;
+                list[j % kPfList] = n;
+                __threadfence_block();
+                *listed = j + 1;
+                return true;
+            };
+            auto entry = [&]() -> uint8_t * {
+                const int sl = issued % kPfKSlots;
+                if (issued >= kPfKSlots &&
+                    !sm100::mbar_wait(&k_free[sl], ((issued / kPfKSlots) - 1) & 1, abort_flag, a.err, lim))
+                    return nullptr;
                 sm100::mbar_arrive_expect_tx(&k_full[sl], 3 * kPfChunk);
-                sm100::tma_load_3d(&maps.kc, &k_full[sl], dst, 0, head, r);
-                sm100::tma_load_3d(&maps.kc, &k_full[sl], dst + kPfChunk, 64, head, r);
-                sm100::tma_load_3d(&maps.kr, &k_full[sl], dst + 2 * kPfChunk, kDc, r, 0);
-                issued = k + 1;
+                ++issued;
+                return smem + kPfOffK + 3 * sl * kPfChunk;
+            };
+            int n = blockIdx.x;
+            bool ok = publish(0, n);
+            for (int j = 0; ok && n < a.items; ++j) {
+                const Item it = item_of(n);
+                n = gridDim.x + atomicAdd(a.counter, 1);
+                if (!publish(j + 1, n)) break;
+                for (int k = -1; ok && k < it.nk && it.nk > 0; ++k) {
+                    uint64_t *bar = &k_full[issued % kPfKSlots];
+                    uint8_t *dst = entry();
+                    if (!(ok = dst != nullptr)) break;
+                    if (k < 0) {
+                        sm100::tma_load_4d(&maps.qn, bar, dst, 0, it.head, it.q0, it.b);
+                        sm100::tma_load_4d(&maps.qn, bar, dst + kPfChunk, 64, it.head, it.q0, it.b);
+                        sm100::tma_load_4d(&maps.qr, bar, dst + 2 * kPfChunk, 0, it.head, it.q0, it.b);
+                    } else {
+                        const int r = it.b * a.lpad + 128 * k;
+                        sm100::tma_load_3d(&maps.kc, bar, dst, 0, it.head, r);
+                        sm100::tma_load_3d(&maps.kc, bar, dst + kPfChunk, 64, it.head, r);
+                        sm100::tma_load_3d(&maps.kr, bar, dst + 2 * kPfChunk, kDc, r, 0);
+                    }
+                }
             }
             if (*abort_flag) {   // let the copies in flight land before the CTA can exit
                 volatile int no_abort = 0;
-                sm100::mbar_wait(q_full, 0, &no_abort, a.err, drain);
-                for (int k = issued - kPfKSlots < 0 ? 0 : issued - kPfKSlots; k < issued; ++k)
-                    sm100::mbar_wait(&k_full[k % kPfKSlots], (k / kPfKSlots) & 1, &no_abort, a.err, drain);
+                for (int g = issued - kPfKSlots < 0 ? 0 : issued - kPfKSlots; g < issued; ++g)
+                    sm100::mbar_wait(&k_full[g % kPfKSlots], (g / kPfKSlots) & 1, &no_abort, a.err, drain);
             }
         }
     } else if (warp == 6) {
         // ----------------------------------------------------------- V loads
-        if (lane == 0 && nk > 0) {
-            int issued = 0;
-            for (int k = 0; k < nk; ++k) {
-                const int sl = k & 1;
-                if (k >= 2 && !sm100::mbar_wait(&v_free[sl], ((k >> 1) - 1) & 1, abort_flag, a.err, lim)) break;
-                uint8_t *dst = smem + kPfOffV + 2 * sl * kPfChunk;
-                const int r = row0 + 128 * k;
-                sm100::mbar_arrive_expect_tx(&v_full[sl], 2 * kPfChunk);
-                sm100::tma_load_3d(&maps.vc, &v_full[sl], dst, 0, head, r);
-                sm100::tma_load_3d(&maps.vc, &v_full[sl], dst + kPfChunk, 64, head, r);
-                issued = k + 1;
-            }
+        if (lane == 0) {
+            int t = 0;
+            Item it;
+            bool ok = true;
+            for (int j = 0; ok && (ok = item_at(j, 0, it)) && it.nk >= 0; ++j)
+                for (int k = 0; k < it.nk; ++k) {
+                    const int sl = t & 1;
+                    if (t >= 2 && !(ok = sm100::mbar_wait(&v_free[sl], ((t >> 1) - 1) & 1, abort_flag, a.err, lim))) break;
+                    uint8_t *dst = smem + kPfOffV + 2 * sl * kPfChunk;
+                    const int r = it.b * a.lpad + 128 * k;
+                    sm100::mbar_arrive_expect_tx(&v_full[sl], 2 * kPfChunk);
+                    sm100::tma_load_3d(&maps.vc, &v_full[sl], dst, 0, it.head, r);
+                    sm100::tma_load_3d(&maps.vc, &v_full[sl], dst + kPfChunk, 64, it.head, r);
+                    ++t;
+                }
             if (*abort_flag) {
                 volatile int no_abort = 0;
-                for (int k = issued - 2 < 0 ? 0 : issued - 2; k < issued; ++k)
+                for (int k = t - 2 < 0 ? 0 : t - 2; k < t; ++k)
                     sm100::mbar_wait(&v_full[k & 1], (k >> 1) & 1, &no_abort, a.err, drain);
             }
         }
-    } else if (warp == 1 || warp == 7) {
-        // ------------------------------------------------------ MMA issue
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- S MMAs
         if (sm100::elect_one()) {
             const uint32_t idesc_s = sm100::idesc_bf16(128, 128, 0, 0);
-            const uint32_t idesc_o = kHalfV ? sm100::idesc_f16(128, 128, 0, 1) : sm100::idesc_bf16(128, 128, 0, 1);
-            bool ok = nk == 0 || sm100::mbar_wait(q_ready, 0, abort_flag, a.err, lim);
-            if (warp == 1) {
-                // S(k) into buffer k % 2
-                auto issue_s = [&](int k) -> bool {
-                    const int sl = k % kPfKSlots;
-                    if (!sm100::mbar_wait(&k_full[sl], (k / kPfKSlots) & 1, abort_flag, a.err, lim)) return false;
+            int g = 0, t = 0, q = 0;   // ring entries, tiles, items with tiles
+            Item it;
+            bool ok = true;
+            for (int j = 0; ok && (ok = item_at(j, 1, it)) && it.nk >= 0; ++j) {
+                if (it.nk == 0) continue;
+                if (!(ok = sm100::mbar_wait(q_ready, q & 1, abort_flag, a.err, lim))) break;
+                sm100::mbar_arrive(&k_free[g % kPfKSlots]);   // the queries' slot
+                ++g;
+                ++q;
+                for (int k = 0; k < it.nk; ++k, ++g, ++t) {
+                    // S(t) into buffer t % 2, over P(t - 2): that P V must have completed
+                    const int sl = g % kPfKSlots;
+                    ok = (t < 2 || sm100::mbar_wait(&pv_done[t & 1], ((t >> 1) - 1) & 1, abort_flag, a.err, lim)) &&
+                         sm100::mbar_wait(&k_full[sl], (g / kPfKSlots) & 1, abort_flag, a.err, lim);
+                    if (!ok) break;
                     sm100::tc_fence_after();
                     const uint32_t ka = sm100::smem_u32(smem + kPfOffK + 3 * sl * kPfChunk);
 #pragma unroll
                     for (int step = 0; step < 12; ++step)      // q^C 0-63, q^C 64-127, q^R
-                        sm100::umma_ts(tmem + kPfTmS + 128 * (k & 1), tmem + kPfTmQ + 8 * step,
+                        sm100::umma_ts(tmem + kPfTmS + 128 * (t & 1), tmem + kPfTmQ + 8 * step,
                                        sm100::desc_kmajor(ka + (step >> 2) * kPfChunk + (step & 3) * 32, 128,
                                                           sm100::kSw128),
                                        idesc_s, step > 0);
-                    sm100::umma_commit(&s_full[k & 1]);
+                    sm100::umma_commit(&s_full[t & 1]);
                     sm100::umma_commit(&k_free[sl]);
-                    return true;
-                };
-                if (ok && nk > 0) ok = issue_s(0);
-                if (ok && nk > 1) ok = issue_s(1);
-                // S(k+2) overwrites P(k): that P V must have completed
-                for (int k = 0; ok && k + 2 < nk; ++k)
-                    ok = sm100::mbar_wait(&pv_done[k & 1], (k >> 1) & 1, abort_flag, a.err, lim) && issue_s(k + 2);
-            } else {
-                for (int k = 0; ok && k < nk; ++k) {
-                    const int pb = k & 1;
-                    ok = sm100::mbar_wait(&p_full[pb], (k >> 1) & 1, abort_flag, a.err, lim) &&
-                         sm100::mbar_wait(&v_full[pb], (k >> 1) & 1, abort_flag, a.err, lim);
+                }
+            }
+            sm100::umma_commit(done);
+        }
+        __syncwarp();
+    } else if (warp == 7) {
+        // -------------------------------------------------------- P V MMAs
+        if (sm100::elect_one()) {
+            const uint32_t idesc_o = kHalfV ? sm100::idesc_f16(128, 128, 0, 1) : sm100::idesc_bf16(128, 128, 0, 1);
+            int t = 0;
+            Item it;
+            bool ok = true;
+            for (int j = 0; ok && (ok = item_at(j, 2, it)) && it.nk >= 0; ++j)
+                for (int k = 0; k < it.nk; ++k, ++t) {
+                    const int pb = t & 1;
+                    ok = sm100::mbar_wait(&p_full[pb], (t >> 1) & 1, abort_flag, a.err, lim) &&
+                         sm100::mbar_wait(&v_full[pb], (t >> 1) & 1, abort_flag, a.err, lim);
                     if (!ok) break;
                     sm100::tc_fence_after();
                     const uint64_t vd =
@@ -260,27 +342,36 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
                     sm100::umma_commit(&pv_done[pb]);
                     sm100::umma_commit(&v_free[pb]);
                 }
-            }
             sm100::umma_commit(done);
         }
         __syncwarp();
-    } else if (warp >= 2 && warp <= 5) {
+    } else {
         // ------------------------------------------------------ softmax
         // warp w owns TMEM lane quarter w % 4; thread = query row r
         const int qd = warp & 3;
-        const int r = 32 * qd + lane, t = q0 + r;
+        const int r = 32 * qd + lane;
         const uint32_t lane_off = (uint32_t)(32 * qd) << 16;
         const uint32_t tm_s = tmem + lane_off + kPfTmS;
         const uint32_t tm_o = tmem + lane_off + kPfTmO, tm_q = tmem + lane_off + kPfTmQ;
-        const bool has_row = t < a.s;
-        const int nvis = has_row ? L - a.s + t + 1 : 0;   // keys [0, nvis) visible to row t
-        bool ok = true;
-        if (nk > 0) {
-            // this row's query [q^C | rotated q^R] into TMEM (192 bf16 = 96 columns;
-            // rows past the sequence's queries arrive as zeros)
-            ok = sm100::warp_wait(q_full, 0, abort_flag, a.err, lim);
-            const uint32_t qs = sm100::smem_u32(smem + kPfOffK + 3 * (kPfKSlots - 1) * kPfChunk) + r * 128;
-#pragma unroll
+        const uint32_t stage = sm100::smem_u32(smem + kPfOffOut) + qd * 32 * 128;
+        int g = 0, tile = 0;   // ring entries and tiles so far
+        // an item's queries [q^C | rotated q^R] into TMEM (a row: 192 bf16 = 96 columns;
+        // rows past the sequence's queries arrive as zeros)
+        auto next_item = [&](int j, Item &it) -> bool {
+            int n = 0;
+            bool ok = true;
+            if (lane == 0 && (ok = count_wait(listed, j + 1))) {
+                n = list[j % kPfList];
+                __threadfence_block();
+                read_to[3 + qd] = j + 1;
+            }
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            it = item_of(__shfl_sync(0xffffffffu, n, 0));
+            if (it.nk <= 0) return true;
+            const int sl = g % kPfKSlots;
+            if (!sm100::warp_wait(&k_full[sl], (g / kPfKSlots) & 1, abort_flag, a.err, lim)) return false;
+            const uint32_t qs = sm100::smem_u32(smem + kPfOffK + 3 * sl * kPfChunk) + r * 128;
+#pragma unroll 1
             for (int c = 0; c < 3; ++c) {
                 uint4 v[8];
 #pragma unroll
@@ -291,112 +382,127 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
             sm100::tc_fence_before();
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(q_ready);
-        }
-        float m_run = -INFINITY, l_run = 0.f;
-        for (int k = 0; ok && k < nk; ++k) {
-            const int pb = k & 1;
-            ok = sm100::warp_wait(&s_full[pb], (k >> 1) & 1, abort_flag, a.err, lim);
-            if (!ok) break;
-            sm100::tc_fence_after();
-            uint32_t x[128];
-#pragma unroll
-            for (int c = 0; c < 128; c += 32) sm100::tmem_ld32(tm_s + 128 * pb + c, x + c);
-            sm100::tmem_wait_ld();
-            const int key0 = 128 * k;
-            if (key0 + 128 > nvis) {
-#pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if (key0 + c >= nvis) x[c] = __float_as_uint(-INFINITY);
-            }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 128; c += 4)
-                mx = fmaxf(mx, fmaxf(fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
-                                     fmaxf(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]))));
-            const float mt = mx * a.scale_log2;
-            const bool grow = (mt != -INFINITY) && (m_run == -INFINITY || mt > m_run + kRescaleThreshold);
-            const bool rescale = grow && m_run != -INFINITY;
-            const float m_new = grow ? mt : m_run;
-            const float corr = rescale ? ex2(m_run - m_new) : 1.f;
-            l_run *= corr;
-            m_run = m_new;
-            float mu = (m_run == -INFINITY) ? 0.f : m_run;
-            if (kHalfV) mu -= kPfHalfShift;
-            float lsum = 0.f;
-#pragma unroll
-            for (int c = 0; c < 64; ++c) {
-                const float p0 = ex2(fmaf(__uint_as_float(x[2 * c]), a.scale_log2, -mu));
-                const float p1 = ex2(fmaf(__uint_as_float(x[2 * c + 1]), a.scale_log2, -mu));
-                lsum += p0 + p1;
-                x[c] = kHalfV ? pack_half2(p0, p1) : pack_bf162(p0, p1);
-            }
-            l_run += lsum;
-            // P(k) over the first 64 columns of S(k), already read by this thread
-            sm100::tmem_st32(tm_s + 128 * pb, x);
-            sm100::tmem_st32(tm_s + 128 * pb + 32, x + 32);
-            if (__any_sync(0xffffffffu, rescale)) {
-                // O holds the tiles before k: let P(k-1) V_{k-1} retire, then
-                // scale this thread's row in place
-                ok = sm100::warp_wait(&pv_done[(k - 1) & 1], ((k - 1) >> 1) & 1, abort_flag, a.err, lim);
+            g += 1 + it.nk;
+            return true;
+        };
+        Item it, nx;
+        bool ok = next_item(0, it);
+        for (int j = 0; ok && it.nk >= 0; ++j, it = nx) {
+            const int t = it.q0 + r;
+            const bool has_row = t < a.s;
+            const int nvis = has_row ? it.L - a.s + t + 1 : 0;   // keys [0, nvis) visible to row t
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int k = 0; k < it.nk; ++k, ++tile) {
+                const int pb = tile & 1;
+                ok = sm100::warp_wait(&s_full[pb], (tile >> 1) & 1, abort_flag, a.err, lim);
                 if (!ok) break;
                 sm100::tc_fence_after();
+                uint32_t x[128];
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) sm100::tmem_ld32(tm_s + 128 * pb + c, x + c);
+                sm100::tmem_wait_ld();
+                const int key0 = 128 * k;
+                if (key0 + 128 > nvis) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (key0 + c >= nvis) x[c] = __float_as_uint(-INFINITY);
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 128; c += 4)
+                    mx = fmaxf(mx, fmaxf(fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
+                                         fmaxf(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]))));
+                const float mt = mx * a.scale_log2;
+                const bool grow = (mt != -INFINITY) && (m_run == -INFINITY || mt > m_run + kRescaleThreshold);
+                const bool rescale = grow && m_run != -INFINITY;
+                const float m_new = grow ? mt : m_run;
+                const float corr = rescale ? ex2(m_run - m_new) : 1.f;
+                l_run *= corr;
+                m_run = m_new;
+                float mu = (m_run == -INFINITY) ? 0.f : m_run;
+                if (kHalfV) mu -= kPfHalfShift;
+                float lsum = 0.f;
+#pragma unroll
+                for (int c = 0; c < 64; ++c) {
+                    const float p0 = ex2(fmaf(__uint_as_float(x[2 * c]), a.scale_log2, -mu));
+                    const float p1 = ex2(fmaf(__uint_as_float(x[2 * c + 1]), a.scale_log2, -mu));
+                    lsum += p0 + p1;
+                    x[c] = kHalfV ? pack_half2(p0, p1) : pack_bf162(p0, p1);
+                }
+                l_run += lsum;
+                // P(k) over the first 64 columns of S(k), already read by this thread
+                sm100::tmem_st32(tm_s + 128 * pb, x);
+                sm100::tmem_st32(tm_s + 128 * pb + 32, x + 32);
+                if (__any_sync(0xffffffffu, rescale)) {
+                    // O holds the tiles before k: let P(k-1) V_{k-1} retire, then
+                    // scale this thread's row in place
+                    ok = sm100::warp_wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort_flag, a.err, lim);
+                    if (!ok) break;
+                    sm100::tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t ov[32];
+                    for (int c = 0; c < 128; c += 32) {
+                        uint32_t ov[32];
+                        sm100::tmem_ld32(tm_o + c, ov);
+                        sm100::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
+                        sm100::tmem_st32(tm_o + c, ov);
+                    }
+                }
+                sm100::tmem_wait_st();
+                sm100::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) sm100::mbar_arrive(&p_full[pb]);
+            }
+            // every S of the item has been read: the next item's queries go in now, so
+            // that its first logits are formed during this epilogue
+            ok = ok && next_item(j + 1, nx);
+            if (!ok) break;
+            // epilogue: O / l as bf16, 64 columns at a time staged with 128-byte swizzle
+            // and stored with TMA by each warp for itself
+            if (it.nk > 0) {
+                ok = sm100::warp_wait(&pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort_flag, a.err, lim);
+                if (!ok) break;
+                sm100::tc_fence_after();
+            }
+            const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+            const float vf = kHalfV ? exp2_int(half_exponent(a.max_bits)) : 1.f;
+            auto o_of = [&](uint32_t x) { return kHalfV ? __uint_as_float(x) * inv * vf : __uint_as_float(x) * inv; };
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t ov[32];
+                if (it.nk > 0) {
                     sm100::tmem_ld32(tm_o + c, ov);
                     sm100::tmem_wait_ld();
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
-                    sm100::tmem_st32(tm_o + c, ov);
+                    for (int e = 0; e < 32; ++e) ov[e] = 0u;
                 }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int unit = ((c & 63) >> 3) + q;        // 16-byte unit of the 128-byte row
+                    st_shared_v4(stage + lane * 128 + ((unit ^ (lane & 7)) << 4),
+                                 make_uint4(pack_bf162(o_of(ov[8 * q]), o_of(ov[8 * q + 1])),
+                                            pack_bf162(o_of(ov[8 * q + 2]), o_of(ov[8 * q + 3])),
+                                            pack_bf162(o_of(ov[8 * q + 4]), o_of(ov[8 * q + 5])),
+                                            pack_bf162(o_of(ov[8 * q + 6]), o_of(ov[8 * q + 7]))));
+                }
+                if ((c & 32) == 0) continue;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && it.q0 + 32 * qd < a.s) {
+                    sm100::tma_store_4d(&maps.out, smem + kPfOffOut + qd * 32 * 128, c & 64, it.head, it.q0 + 32 * qd, it.b);
+                    sm100::tma_store_commit();
+                    sm100::tma_store_wait_read();
+                }
+                __syncwarp();
             }
-            sm100::tmem_wait_st();
+            if (a.out_lse && has_row)
+                a.out_lse[((long long)it.b * a.s + t) * a.H + it.head] =
+                    l_run > 0.f ? (m_run + __log2f(l_run) - (kHalfV ? kPfHalfShift : 0.f)) * kLn2 : -INFINITY;
+            // O is read: the next item's first P V may overwrite it
             sm100::tc_fence_before();
             __syncwarp();
-            if (lane == 0) sm100::mbar_arrive(&p_full[pb]);
-        }
-        // epilogue: O / l as bf16, staged over K slot 0 (free once the last
-        // P V completed, which follows every S MMA) as two [128 rows][128 B]
-        // chunks with 128-byte swizzle, stored with TMA
-        if (ok && nk > 0) {
-            ok = sm100::warp_wait(&pv_done[(nk - 1) & 1], ((nk - 1) >> 1) & 1, abort_flag, a.err, lim);
-            sm100::tc_fence_after();
-        }
-        const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-        const float vf = kHalfV ? exp2_int(half_exponent(a.max_bits)) : 1.f;
-        auto o_of = [&](uint32_t x) { return kHalfV ? __uint_as_float(x) * inv * vf : __uint_as_float(x) * inv; };
-        uint8_t *stage = smem + kPfOffK;
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-            uint32_t ov[32];
-            if (ok && nk > 0) {
-                sm100::tmem_ld32(tm_o + c, ov);
-                sm100::tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) ov[e] = 0u;
-            }
-            uint8_t *chunk = stage + (c >> 6) * kPfChunk;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int unit = ((c & 63) >> 3) + q;        // 16-byte unit of the 128-byte row
-                *reinterpret_cast<uint4 *>(chunk + r * 128 + ((unit ^ (r & 7)) << 4)) =
-                    make_uint4(pack_bf162(o_of(ov[8 * q]), o_of(ov[8 * q + 1])),
-                               pack_bf162(o_of(ov[8 * q + 2]), o_of(ov[8 * q + 3])),
-                               pack_bf162(o_of(ov[8 * q + 4]), o_of(ov[8 * q + 5])),
-                               pack_bf162(o_of(ov[8 * q + 6]), o_of(ov[8 * q + 7])));
-            }
-        }
-        if (a.out_lse && has_row)
-            a.out_lse[((long long)b * a.s + t) * a.H + head] =
-                l_run > 0.f ? (m_run + __log2f(l_run) - (kHalfV ? kPfHalfShift : 0.f)) * kLn2 : -INFINITY;
-        fence_proxy_async_smem();
-        asm volatile("bar.sync 1, 128;" ::: "memory");     // the 4 softmax warps
-        if (warp == 2 && lane == 0) {
-            sm100::tma_store_4d(&maps.out, stage, 0, head, q0, b);
-            sm100::tma_store_4d(&maps.out, stage + kPfChunk, 64, head, q0, b);
-            sm100::tma_store_commit();
-            sm100::tma_store_wait_read();
         }
     }
 
