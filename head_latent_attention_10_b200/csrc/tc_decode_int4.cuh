@@ -24,10 +24,10 @@
 //   - Eight converter warps (8-15) read a page's codes and scales from global
 //     memory into registers one page ahead, and widen them into the tile layout
 //     when its stage is free.  No copy of the codes passes through shared
-//     memory, which the three stages fill.
-//     Each register is loaded again in place right after its use and touched a page
-//     later: a copy of one in between would wait for its load (293 against 223 us on
-//     128 sequences x 128 heads x 4,096 tokens).
+//     memory, which the three stages fill.  Each register is loaded again in place
+//     right after its use and touched a page later: a copy of one in between would
+//     wait for its load (293 against 223 us on 128 sequences x 128 heads x 4,096
+//     tokens, before the later steps).
 //   - Warp 0 walks the range's tile list and publishes {page, sequence, tile}
 //     entries in shared memory (and warms L2), so that no other warp holds the
 //     walk's state: the loops of all roles together stay small, because the
@@ -45,6 +45,13 @@
 //
 // Rows past a sequence's end get logit -inf, so weight 0; any pattern a page
 // can hold is finite, so their latents add exactly 0 and need no zeroing.
+//
+// Measured (call, back to back): 128 sequences x 128 heads x 4,096 tokens 203 us (146
+// GFLOP: 88 us at the pipe's full rate, 126 us at M=64; the pipe is active in 70 % of
+// the cycles), 64 x 16 heads x 4,096 65 us (87 MB: 13 us), one sequence of 16 heads
+// and 256 tokens 17 us.  A tile takes about 2,700 cycles: its 2,166 of MMAs and gaps
+// before each group of them.  A sequence's end inside a range takes about 14,000
+// cycles, of which the next queries are 4,600 and the output 8,400.
 //
 // Work split and partial results are the bf16 decode's (plan_range); every cut
 // sequence is merged by dec4_combine_kernel.  Every wait is bounded; one that gives

@@ -11,7 +11,7 @@
 //
 // With many queries per sequence the expanded form costs fewer flops than the
 // absorbed one (2 (192 + 128) per query, key and head against 2 (576 + 512)),
-// and the step is bound by the tensor cores: a FlashAttention-style loop on
+// and the step is bound by the tensor cores: an online-softmax loop on
 // tcgen05.  An item is (128-query tile, head i, sequence b), the tile as MMA
 // M = 128; it streams 128-key tiles of K = [K^C | k^R] and V^C:
 //   S(k) = Q K_k^T    N=128, K=192: 12 MMAs, Q read from TMEM
@@ -53,8 +53,9 @@
 //
 // kHalfV: V^C and P are f16 instead of bf16 (the 4-bit cache's prefill).  The
 // latents there are read exactly, and the two roundings to 8 bits of P and V^C
-// would be two thirds of the output's error (its relative rms 0.0029 against
-// 0.0017 for the output's own rounding to bf16).  f16 needs its range kept: V^C
+// would be two thirds of the output's squared error (its relative rms 0.0029, so
+// 0.0021, of which the output's own rounding to bf16 is 0.0017; the rest is the
+// rounding of K^C and the queries).  f16 needs its range kept: V^C
 // is stored times 2^-e, with e from the largest latent and weight magnitudes
 // (prefill_prepare_kernel), so that none overflows whatever the weights, and P
 // is formed as 2^7 p (p <= 2^8), which leaves weights down to 2^-21 their 11
