@@ -168,19 +168,20 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 }
 
 // C = A B on tcgen05; `c` is the output tensor map of the staged (TMA store)
-// epilogue, unused by the others.
-template <int BN, bool kBmn, class Epi, bool kAmn = false, int kStages = kGemmStages>
+// epilogue, unused by the others.  With b1 and c1, A B1 as well (Z = 1).
+template <int BN, bool kBmn, class Epi, bool kAmn = false, int kStages = kGemmStages, bool kPair = false>
 cudaError_t launch_tc_gemm(const CUtensorMap &a, const CUtensorMap &b, int M, int N, int K, int Z, const Epi &epi,
-                           uint32_t *err, cudaStream_t st, const CUtensorMap *c = nullptr)
+                           uint32_t *err, cudaStream_t st, const CUtensorMap *c = nullptr,
+                           const CUtensorMap *b1 = nullptr, const CUtensorMap *c1 = nullptr)
 {
     using S = GemmSmem<BN, kStages>;
-    auto kern = tc_gemm_kernel<BN, kBmn, Epi, kAmn, kStages>;
+    auto kern = tc_gemm_kernel<BN, kBmn, Epi, kAmn, kStages, kPair>;
     static std::atomic<bool> attr_set[kMaxDevices];
     const cudaError_t e = ensure_smem_attr(kern, S::BYTES, attr_set);
     if (e != cudaSuccess) return e;
-    dim3 grid((N + BN - 1) / BN, (M + 127) / 128, Z);
-    const cudaError_t le = launch_pdl(kern, grid, dim3(kGemmThreads), S::BYTES, st, a, b, c ? *c : a, M, N, K, epi,
-                                      err, kWaitLimitNs);
+    dim3 grid((N + BN - 1) / BN, (M + 127) / 128, kPair ? 2 : Z);
+    const cudaError_t le = launch_pdl(kern, grid, dim3(kGemmThreads), S::BYTES, st, a, b, c ? *c : a, b1 ? *b1 : b,
+                                      c1 ? *c1 : a, M, N, K, epi, err, kWaitLimitNs);
     count_launch();
     return le;
 }
@@ -496,20 +497,19 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
         q_rot, rope_table(dims), (const uint4 *)w_uv, max_bits, err);
     count_launch();
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-    // More tiles than SMs: two stages, so that two CTAs of an SM overlap one's
-    // start and epilogue with the other's products (73 us against 98 at 4,096 rows
-    // x 128 heads); fewer: four, which hide a lone CTA's loads (9.4 against 11.1 us
-    // at 1,152 rows x 16 heads).
-    auto expand = [&](const CUtensorMap &w_map, const auto &epi, const CUtensorMap &out_map) {
-        using Epi = std::decay_t<decltype(epi)>;
-        return (long long)((M + 127) / 128) * ((H * kDh + 255) / 256) > sm_count()
-            ? launch_tc_gemm<256, false, Epi, false, 2>(ma, w_map, M, H * kDh, kDc, 1, epi, err, strm, &out_map)
-            : launch_tc_gemm<256, false, Epi>(ma, w_map, M, H * kDh, kDc, 1, epi, err, strm, &out_map);
-    };
-    using VEpi = std::conditional_t<kHalfV, TcEpiTmaStoreHalf, TcEpiTmaStore>;
-    VEpi v_epi{};
-    if constexpr (kHalfV) v_epi.max_bits = max_bits;
-    if (expand(muk, TcEpiTmaStore{}, skc) != cudaSuccess || expand(muv, v_epi, svc) != cudaSuccess) return MLA_ERR_CUDA;
+    // Both expansions in one launch: a short chunk's tiles of one leave half of the
+    // SMs free.  More tiles than SMs: two stages, so that two CTAs of an SM overlap
+    // one's start and epilogue with the other's products (73 us a product against 98
+    // at 4,096 rows x 128 heads); fewer: four, which hide a lone CTA's loads (9.4
+    // against 11.1 us at 1,152 rows x 16 heads).
+    const TcEpiTmaStorePair epi{kHalfV ? max_bits : nullptr};
+    const cudaError_t ge =
+        2ll * ((M + 127) / 128) * ((H * kDh + 255) / 256) > sm_count()
+            ? launch_tc_gemm<256, false, TcEpiTmaStorePair, false, 2, true>(ma, muk, M, H * kDh, kDc, 1, epi, err, strm,
+                                                                            &skc, &muv, &svc)
+            : launch_tc_gemm<256, false, TcEpiTmaStorePair, false, kGemmStages, true>(ma, muk, M, H * kDh, kDc, 1, epi, err,
+                                                                                      strm, &skc, &muv, &svc);
+    if (ge != cudaSuccess) return MLA_ERR_CUDA;
     PrefillArgs pa;
     pa.seq_lens = seq_lens;
     pa.s = s;
@@ -528,9 +528,10 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
     if (ensure_smem_attr(tc_prefill_kernel<kHalfV>, kPfSmem, attr_set) != cudaSuccess) return MLA_ERR_CUDA;
     const int ctas = sm_count();
     if (ctas <= 0) return MLA_ERR_CUDA;
-    tc_prefill_kernel<kHalfV><<<pa.items < ctas ? pa.items : ctas, kPfThreads, kPfSmem, strm>>>(pm, pa);
+    const cudaError_t ae = launch_pdl(tc_prefill_kernel<kHalfV>, dim3(pa.items < ctas ? pa.items : ctas), dim3(kPfThreads),
+                                      kPfSmem, strm, pm, pa);
     count_launch();
-    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    if (ae != cudaSuccess) return MLA_ERR_CUDA;
     if (flags & MLA_SYNC_CHECK) {
         uint32_t h = 0;
         if (cudaMemcpyAsync(&h, err, sizeof h, cudaMemcpyDeviceToHost, strm) != cudaSuccess ||

@@ -33,7 +33,7 @@ struct GemmSmem {
     static constexpr int TMEM_COLS = BN <= 32 ? 32 : (BN <= 64 ? 64 : (BN <= 128 ? 128 : 256));
 };
 
-// 2^n, |n| <= 126, and the exponent e of TcEpiTmaStoreHalf: a pattern with
+// 2^n, |n| <= 126, and the exponent e of TcEpiTmaStorePair: a pattern with
 // exponent field x stands for less than 2^(x - 126), so the bound is
 // 2^(9 + x - 126 + y - 126).
 __device__ __forceinline__ float exp2_int(int n) { return __uint_as_float((uint32_t)(127 + n) << 23); }
@@ -43,12 +43,17 @@ __device__ __forceinline__ int half_exponent(const uint32_t *max_bits)
     return min(max(e, -126), 126);
 }
 
-template <int BN, bool kBmn, class Epi, bool kAmn = false, int kStages = kGemmStages>
+// kPair: two products of one A in one launch, blockIdx.z = 1 with the second B and
+// C maps (Z = 1).
+template <int BN, bool kBmn, class Epi, bool kAmn = false, int kStages = kGemmStages, bool kPair = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-               const __grid_constant__ CUtensorMap mapC, int M, int N, int K, Epi epi, uint32_t *err,
+tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB0,
+               const __grid_constant__ CUtensorMap mapC0, const __grid_constant__ CUtensorMap mapB1,
+               const __grid_constant__ CUtensorMap mapC1, int M, int N, int K, Epi epi, uint32_t *err,
                unsigned long long limit_ns)
 {
+    const bool second = kPair && blockIdx.z == 1;
+    const CUtensorMap &mapB = second ? mapB1 : mapB0, &mapC = second ? mapC1 : mapC0;
     using S = GemmSmem<BN, kStages>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -59,7 +64,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n0 = blockIdx.x * BN, m0 = blockIdx.y * 128, z = blockIdx.z;
+    const int n0 = blockIdx.x * BN, m0 = blockIdx.y * 128, z = kPair ? 0 : blockIdx.z;
     const int nk = K / 64;
 
     if (threadIdx.x == 0) {
@@ -152,7 +157,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
             // [128 rows][128 B] (128-byte swizzle), stored with TMA by one
             // thread: whole lines rather than 32 rows' pieces per instruction
             const int r = q * 32 + lane;
-            const float f = epi.factor();
+            const float f = epi.factor(second);
 #pragma unroll 1
             for (int c = 0; c < BN; c += 32) {
                 uint32_t v[32];
@@ -220,21 +225,25 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
 struct TcEpiTmaStore {
     static constexpr bool kStaged = true;
     int split_n = 0;
-    __device__ float factor() const { return 1.f; }
+    __device__ float factor(bool) const { return 0.f; }
     __device__ uint32_t pack(float lo, float hi, float) const { return pack_bf162(lo, hi); }
     __device__ void operator()(int, int, int, const float *) const {}
 };
 
-// The same with f16 outputs scaled by 2^-e, for products of operands whose
-// largest finite magnitudes' bf16 patterns are max_bits[0] and max_bits[1]:
-// with K = 512 no product is beyond 2^9 times both, and e (half_exponent) is
-// the least that keeps that bound at 2^15.
-struct TcEpiTmaStoreHalf {
+// The same for a pair of products, the second's outputs (where max_bits is given)
+// f16 scaled by 2^-e, for operands whose largest finite magnitudes' bf16 patterns
+// are max_bits[0] and max_bits[1]: with K = 512 no product is beyond 2^9 times
+// both, and e (half_exponent) is the least that keeps that bound at 2^15.
+struct TcEpiTmaStorePair {
     static constexpr bool kStaged = true;
     const uint32_t *max_bits;
     int split_n = 0;
-    __device__ float factor() const { return exp2_int(-half_exponent(max_bits)); }
-    __device__ uint32_t pack(float lo, float hi, float f) const { return pack_half2(lo * f, hi * f); }
+    // (0: bf16)
+    __device__ float factor(bool second) const { return second && max_bits ? exp2_int(-half_exponent(max_bits)) : 0.f; }
+    __device__ uint32_t pack(float lo, float hi, float f) const
+    {
+        return f != 0.f ? pack_half2(lo * f, hi * f) : pack_bf162(lo, hi);
+    }
     __device__ void operator()(int, int, int, const float *) const {}
 };
 
