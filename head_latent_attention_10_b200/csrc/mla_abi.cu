@@ -370,7 +370,12 @@ mla_status_t run_int4_decode(const mla_dims_t *dims, const void *q_abs, const vo
     const int groups = dec_groups(H, s), ranges = decode_int4_ranges(groups, B, max_blocks);
     if (ranges <= 0) return MLA_ERR_CUDA;
     // the error word, the plan and its count
-    if (cudaMemsetAsync(ws, 0, w.off_zero_end, strm) != cudaSuccess) return MLA_ERR_CUDA;
+    const long long words = w.off_zero_end / 4, most_clear = sm_count();
+    cudaError_t e = launch_pdl(dec4_clear_kernel,
+                               dim3((unsigned)(words / 1024 < most_clear ? words / 1024 + 1 : most_clear)), dim3(256), 0,
+                               strm, (int *)ws, words);
+    count_launch();
+    if (e != cudaSuccess) return MLA_ERR_CUDA;
     int *cflags = (int *)(ws + w.off_flags);
     Dec4Args da;
     da.q_abs = (const bf16 *)q_abs;
@@ -394,7 +399,7 @@ mla_status_t run_int4_decode(const mla_dims_t *dims, const void *q_abs, const vo
     da.H = H;
     da.B = B;
     da.groups = groups;
-    cudaError_t e = launch_pdl(tc_decode_int4_kernel, dim3(ranges * groups), dim3(kD4Threads), kD4Smem, strm, da);
+    e = launch_pdl(tc_decode_int4_kernel, dim3(ranges * groups), dim3(kD4Threads), kD4Smem, strm, da);
     count_launch();
     if (e != cudaSuccess) return MLA_ERR_CUDA;
     const long long rows = (long long)B * s * H, most = 8ll * sm_count();

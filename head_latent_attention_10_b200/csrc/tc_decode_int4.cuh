@@ -118,6 +118,16 @@ __device__ __noinline__ uint64_t d4_wait_tick(uint64_t t0, volatile int *abort, 
     return t0;
 }
 
+// The call's error word, plan and counts cleared.  A kernel rather than a memset,
+// because a memset ends before the next kernel is launched: here the decode's set-up
+// overlaps it.
+__global__ void __launch_bounds__(256) dec4_clear_kernel(int *p, long long n)
+{
+    sm100::pdl_trigger();
+    sm100::pdl_wait();
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) p[i] = 0;
+}
+
 #define D4_RARE(x) __builtin_expect(!!(x), 0)
 
 __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec4Args a)
