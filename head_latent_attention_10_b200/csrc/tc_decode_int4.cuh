@@ -48,8 +48,8 @@
 //
 // Measured (call, back to back): 128 sequences x 128 heads x 4,096 tokens 203 us (146
 // GFLOP: 88 us at the pipe's full rate, 126 us at M=64; the pipe is active in 70 % of
-// the cycles), 64 x 16 heads x 4,096 65 us (87 MB: 13 us), one sequence of 16 heads
-// and 256 tokens 17 us.  A tile takes about 2,700 cycles: its 2,166 of MMAs and gaps
+// the cycles), 64 x 16 heads x 4,096 62 us (87 MB: 13 us), one sequence of 16 heads
+// and 256 tokens 15 us.  A tile takes about 2,700 cycles: its 2,166 of MMAs and gaps
 // before each group of them.  A sequence's end inside a range takes about 14,000
 // cycles, of which the next queries are 4,600 and the output 8,400.
 //
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
 //     the batch has few rows: one CTA per (row, 128 columns), its eight warps taking
 //     the pieces eight by eight in turn, eight loads in flight each; their sums are
 //     added in warp order.  One sequence of 16 heads and 32,768 tokens (148 pieces):
-//     the call takes 31 us so, 50 us with a warp per row and 128 columns; 4 x 128
+//     the call took 31 us so, 50 us with a warp per row and 128 columns; 4 x 128
 //     heads x 2,000 tokens (16 pieces): 38 us so, 27 us with a warp per row.
 // The weights 2^(lse2_i - max) are kept per warp in shared memory; a warp sums its
 // pieces in range order, so the bits do not change from run to run.
