@@ -492,6 +492,29 @@ def test_prefill_refuses_lengths_it_cannot_hold_and_skips_bad_blocks(M):
     assert err == M.MLA_DEVERR_BLOCK_ID and np.array_equal(got[20:], good[20:])
 
 
+def test_prefill_of_many_short_and_invalid_sequences(M):
+    """More items than SMs, most of one key tile; runs of sequences that are too
+    short for the chunk (zero rows) between and around the others, which keep the
+    formula's results; and a batch with no valid sequence at all."""
+    rng = np.random.default_rng(45)
+    lens = rng.integers(3, 190, 300)
+    cfg = C("many", 16, lens.tolist(), s=3, seed=45)
+    d = W.make_decode_inputs(cfg, with_cache_pages=False)
+    codes, scales = random_cache(d, 45)
+    ref, rlse, tol, tol_lse = plain_prefill(codes, scales, d, cfg)
+    for bad in (np.r_[:120, 150:153, 290:300], np.r_[rng.permutation(300)[:150]], np.r_[1:300], np.r_[:300]):
+        now = lens.astype(np.int32)
+        now[bad] = rng.integers(-1, 3, bad.size)
+        got, lse, err, want, _ = run_prefill(M, cfg, d, codes, scales, int(lens.max()), lens=now)
+        dead = np.zeros(300, bool)
+        dead[bad] = True
+        dead = np.repeat(dead, 3)
+        assert err == M.MLA_DEVERR_SEQ_LEN
+        assert np.all(got[dead] == 0) and np.all(np.isneginf(lse[dead])) and np.all(want[dead] == 0)
+        assert np.all(np.abs(floats(got) - ref)[~dead] <= tol[~dead])
+        assert np.all(np.abs(lse - rlse)[~dead] <= tol_lse[~dead])
+
+
 # --------------------------------------------------------------- all together
 def test_a_served_sequence_end_to_end_eager_on_a_stream_and_in_a_graph(M):
     """A prompt is appended and prefilled, then tokens are appended and decoded
