@@ -403,9 +403,13 @@ mla_status_t run_int4_decode(const mla_dims_t *dims, const void *q_abs, const vo
     count_launch();
     if (e != cudaSuccess) return MLA_ERR_CUDA;
     const long long rows = (long long)B * s * H, most = 8ll * sm_count();
-    const bool few = rows <= kD4FewRows && ranges >= (long long)kD4ManyPieces * B;
-    const long long blocks = few ? rows * 4 : (rows + kD4CombineWarps - 1) / kD4CombineWarps;
-    e = launch_pdl(few ? dec4_combine_kernel<true> : dec4_combine_kernel<false>,
+    const int mode = rows <= kD4FewRows && ranges >= (long long)kD4ManyPieces * B   ? 2
+                     : rows <= kD4SomeRows && ranges >= (long long)kD4SomePieces * B ? 1
+                                                                                     : 0;
+    const long long blocks = mode == 2 ? rows * 4 : ((mode == 1 ? 4 * rows : rows) + kD4CombineWarps - 1) / kD4CombineWarps;
+    e = launch_pdl(mode == 2   ? dec4_combine_kernel<2>
+                   : mode == 1 ? dec4_combine_kernel<1>
+                               : dec4_combine_kernel<0>,
                    dim3((unsigned)(blocks < most ? blocks : most)), dim3(32 * kD4CombineWarps), 0, strm,
                    (const int32_t *)da.plan, (const float *)da.part_o, (const float *)da.part_lse2, B, s, H,
                    (bf16 *)out_latent, out_lse);

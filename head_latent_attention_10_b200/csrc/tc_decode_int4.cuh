@@ -622,24 +622,30 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
 // Sequences cut by range ends are merged by log-sum-exp; sequences one range
 // finished are already in place; query rows with no visible key get a zero
 // latent and lse = -inf.  Only the sequences plan_range lists are visited.
-//   kFew = false: one warp per row, all 512 columns, two pieces' loads in flight.
-//   kFew = true, where a sequence can be cut into kD4ManyPieces pieces or more and
-//     the batch has few rows: one CTA per (row, 128 columns), its eight warps taking
-//     the pieces eight by eight in turn, eight loads in flight each; their sums are
-//     added in warp order.  One sequence of 16 heads and 32,768 tokens (148 pieces):
-//     the call took 31 us so, 50 us with a warp per row and 128 columns; 4 x 128
-//     heads x 2,000 tokens (16 pieces): 38 us so, 27 us with a warp per row.
+//   kMode 0: one warp per row, all 512 columns, two pieces' loads in flight.
+//   kMode 1, where a sequence may be cut into kD4SomePieces pieces or more and the
+//     batch has at most kD4SomeRows rows: one warp per row and 128 columns, eight pieces
+//     in flight.  Two sequences of 128 heads x 20,000 tokens (37 pieces): the call
+//     takes 41.4 us so, 47.9 with mode 0; 8 x 16 heads x 1,000 (8 pieces) 19.0 against
+//     19.6; 32 x 16 heads x 800 (4 pieces) 22.3 against 21.3.
+//   kMode 2, where it may be cut into kD4ManyPieces and there are at most kD4FewRows
+//     rows: one CTA per row and 128 columns, its eight warps taking the pieces eight by
+//     eight in turn; their sums are added in warp order.  One sequence of 16 heads and
+//     32,768 tokens (148 pieces): 26.3 us so, 45.1 with mode 1; 4 x 16 heads x 8,000 (37
+//     pieces) 24.0 against 27.1; 2 x 128 heads x 5,000 (256 rows) 31.8 against 28.2.
 // The weights 2^(lse2_i - max) are kept per warp in shared memory; a warp sums its
 // pieces in range order, so the bits do not change from run to run.
 constexpr int kD4CombineWarps = 8;
-constexpr int kD4ManyPieces = 64, kD4FewRows = 512;
+constexpr int kD4SomePieces = 5, kD4SomeRows = 1024;
+constexpr int kD4ManyPieces = 28, kD4FewRows = 192;
 
-template <bool kFew>
+template <int kMode>
 __global__ void __launch_bounds__(32 * kD4CombineWarps)
 dec4_combine_kernel(const int32_t *plan, const float *part_o, const float *part_lse2, int B, int s, int H,
                     bf16 *__restrict__ out, float *__restrict__ out_lse)
 {
-    constexpr int kQuads = kFew ? 1 : 4;      // 128-column quarters of a warp
+    constexpr bool kParts = kMode > 0, kFew = kMode == 2;
+    constexpr int kQuads = kParts ? 1 : 4;    // 128-column quarters of a warp
     constexpr int kAhead = 8 / kQuads;        // pieces in flight
     __shared__ float weight[kD4CombineWarps][kMaxRanges];
     __shared__ float4 sums[kFew ? kD4CombineWarps : 1][32];
@@ -648,10 +654,10 @@ dec4_combine_kernel(const int32_t *plan, const float *part_o, const float *part_
     const int qv = __ldcg(plan), pw = __ldcg(plan + 3), nlist = __ldcg(plan + 5 + B);
     const int4 *list = reinterpret_cast<const int4 *>(plan + plan_list_off(B));
     const unsigned rows = s * H, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const unsigned items = nlist * rows * (kFew ? 4 : 1);
+    const unsigned items = nlist * rows * (kParts ? 4 : 1);
     const unsigned step = kFew ? gridDim.x : gridDim.x * kD4CombineWarps;
     for (unsigned it = kFew ? blockIdx.x : blockIdx.x * kD4CombineWarps + warp; it < items; it += step) {
-        const unsigned part = kFew ? it & 3 : 0, line = kFew ? it >> 2 : it;
+        const unsigned part = kParts ? it & 3 : 0, line = kParts ? it >> 2 : it;
         const unsigned li = line / rows, row = line - li * rows;
         const int4 seq = __ldcg(list + li);
         const int b = seq.x, va = seq.y, tb = seq.z, L = seq.w;

@@ -118,6 +118,9 @@ DECODE = [
     C("h64_many_splits", 64, [2500, 1100], seed=8),
     C("h32_contiguous", 32, [257, 64], paged=False, seed=9),
     C("h16_many_short", 16, list(range(1, 180)), seed=10),
+    C("h16_one_long", 16, [9000], seed=11),
+    C("h32_two_queries_long", 32, [4200, 2, 3900], s=2, seed=12),
+    C("h128_some_pieces", 128, [1700, 1], seed=13),
 ]
 
 
