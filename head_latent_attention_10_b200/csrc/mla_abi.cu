@@ -232,13 +232,13 @@ TcWs tc_ws(int H, int s, int B)
 // [B s][H][64]][K^C [B Lpad][H][128]][V^C [B Lpad][H][128]]
 struct PfWs {
     size_t off_rows, off_qr, off_kc, off_vc, total;
-    int lpad;
+    long long lpad;   // max_seq_len rounded up to 128 rows (which may pass 2^31)
 };
 
 PfWs pf_ws(int H, int B, int s, int max_seq_len)
 {
     PfWs w;
-    w.lpad = (max_seq_len + 127) / 128 * 128;
+    w.lpad = ((long long)max_seq_len + 127) / 128 * 128;
     const size_t rows = (size_t)B * w.lpad;
     w.off_rows = kWsAlign;
     w.off_qr = align_up(w.off_rows + rows * kRow * 2, kWsAlign);
@@ -445,6 +445,15 @@ mla_status_t run_simple_decode(const mla_dims_t *dims, const void *q_abs, const 
     return MLA_OK;
 }
 
+// Sizes the prefill holds: the expansions' grid has a row tile of 128 padded rows
+// (a sequence's are max_seq_len's rounded up) in its second dimension, and rows of
+// queries are counted in 32 bits.
+bool prefill_sizes_ok(long long B, long long s, long long H, long long max_seq_len)
+{
+    return (max_seq_len + 127) / 128 <= 65535 && B * ((max_seq_len + 127) / 128) <= 65535 &&
+           B * s * H <= (1ll << 31) - 1;
+}
+
 // The prefill over cache rows read through `cache` (argument checks are the
 // caller's).
 template <bool kHalfV, class Rows>
@@ -456,10 +465,8 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
 {
     const int H = dims->num_heads;
     const PfWs w = pf_ws(H, B, s, max_seq_len);
+    const int lpad = (int)w.lpad, M = (int)(B * w.lpad);
     if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
-    const long long rows_total = (long long)B * w.lpad;
-    if (rows_total > (1ll << 31) - 1 || (long long)B * s * H > (1ll << 31) - 1) return MLA_ERR_UNSUPPORTED;
-    const int M = (int)rows_total;
     char *ws = (char *)workspace;
     uint32_t *err = (uint32_t *)ws, *max_bits = err + 2;
     bf16 *rows = (bf16 *)(ws + w.off_rows), *q_rot = (bf16 *)(ws + w.off_qr);
@@ -500,9 +507,9 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
         pm.vc = mvc;
     }
     if (cudaMemsetAsync(err, 0, 8 * sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
-    const PrepareBlocks pb(B, w.lpad, s, H, kHalfV);
+    const PrepareBlocks pb(B, lpad, s, H, kHalfV);
     prefill_prepare_kernel<Rows, kHalfV><<<pb.rows + pb.rope + pb.weights, 256, 0, strm>>>(
-        cache, pb, num_blocks, block_table, max_blocks, seq_lens, s, H, w.lpad, l_cap, rows, (const bf16 *)q_rope, q_pos,
+        cache, pb, num_blocks, block_table, max_blocks, seq_lens, s, H, lpad, l_cap, rows, (const bf16 *)q_rope, q_pos,
         q_rot, rope_table(dims), (const uint4 *)w_uv, max_bits, err);
     count_launch();
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
@@ -523,7 +530,7 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
     pa.seq_lens = seq_lens;
     pa.s = s;
     pa.H = H;
-    pa.lpad = w.lpad;
+    pa.lpad = lpad;
     pa.l_cap = l_cap;
     pa.scale_log2 = softmax_scale(dims) * kLog2e;
     pa.out_lse = out_lse;
@@ -843,6 +850,7 @@ mla_status_t mla_prefill(const mla_dims_t *dims, const void *q_nope, const void 
     if (!aligned16(q_nope) || !aligned16(q_rope) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned16(cache) ||
         !aligned16(out))
         return MLA_ERR_INVALID_ARG;
+    if (!prefill_sizes_ok(B, s, dims->num_heads, max_seq_len)) return MLA_ERR_UNSUPPORTED;
     if (!workspace) return MLA_ERR_WORKSPACE;
     return run_prefill<false>(dims, q_nope, q_rope, q_pos, w_uk, w_uv, Bf16Rows{(const bf16 *)cache}, num_blocks, block_table,
                        max_blocks, seq_lens, B, s, max_seq_len, out, out_lse, workspace, ws_bytes, flags,
@@ -990,9 +998,7 @@ mla_status_t mla_prefill_int4(const mla_dims_t *dims, const void *q_nope, const 
     if (!aligned16(q_nope) || !aligned16(q_rope) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned16(codes) ||
         !aligned16(scales) || !aligned16(out))
         return MLA_ERR_INVALID_ARG;
-    // 127: run_prefill rounds max_seq_len up to a multiple of 128; 65535: the
-    // grid's limit on sequences
-    if (!int4_sizes_ok(B, s, dims->num_heads, max_blocks) || max_seq_len > (1ll << 31) - 1 - 127 || B > 65535)
+    if (!int4_sizes_ok(B, s, dims->num_heads, max_blocks) || !prefill_sizes_ok(B, s, dims->num_heads, max_seq_len))
         return MLA_ERR_UNSUPPORTED;
     if (!workspace) return MLA_ERR_WORKSPACE;
     return run_prefill<true>(dims, q_nope, q_rope, q_pos, w_uk, w_uv,

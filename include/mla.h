@@ -307,8 +307,9 @@ size_t mla_prefill_workspace_size(const mla_dims_t *dims, int B, int s, int max_
  *   flags       MLA_SYNC_CHECK
  * A sequence with seq_lens[b] < s, > max_seq_len or > max_blocks * 64 gets
  * zero outputs, lse = -inf and MLA_DEVERR_SEQ_LEN.  B = 0 is a no-op; with
- * B > 0, num_blocks and max_blocks must be at least 1.  Calls that share a
- * workspace must not overlap on the GPU.
+ * B > 0, num_blocks and max_blocks must be at least 1.  B * round_up(max_seq_len,
+ * 128) is at most 65,535 * 128 rows and B * s * num_heads below 2^31
+ * (MLA_ERR_UNSUPPORTED).  Calls that share a workspace must not overlap on the GPU.
  */
 mla_status_t mla_prefill(const mla_dims_t *dims, const void *q_nope, const void *q_rope,
                          const int32_t *q_pos, const void *w_uk, const void *w_uv, const void *cache,
@@ -424,10 +425,9 @@ mla_status_t mla_decode_int4(const mla_dims_t *dims, const void *q_abs, const vo
 /*
  * mla_prefill_int4 -- mla_prefill over the 4-bit cache: the same attention on
  * the rows the cache stands for (the chunk's own rows included: append them
- * first).  Arguments, workspace (mla_prefill_workspace_size), outputs and errors
- * as for mla_prefill, with `codes` and `scales` in place of `cache`; at most
- * 65,535 sequences, and the size limits of mla_decode_int4
- * (MLA_ERR_UNSUPPORTED).  v^C and the softmax weights are rounded to f16 (under a
+ * first).  Arguments, workspace (mla_prefill_workspace_size), outputs, errors and
+ * size limits as for mla_prefill, with `codes` and `scales` in place of `cache`, and
+ * max_blocks * block_size below 2^31 (MLA_ERR_UNSUPPORTED).  v^C and the softmax weights are rounded to f16 (under a
  * power of two that keeps v^C in range) where mla_prefill rounds them to bf16.
  */
 mla_status_t mla_prefill_int4(const mla_dims_t *dims, const void *q_nope, const void *q_rope,
