@@ -228,10 +228,11 @@ TcWs tc_ws(int H, int s, int B)
     return w;
 }
 
-// Prefill workspace: [error word][gathered rows [B Lpad][576]][rotated q^R
-// [B s][H][64]][K^C [B Lpad][H][128]][V^C [B Lpad][H][128]]
+// Prefill workspace: [error word, item counter][operand maxima [B + H]][gathered
+// rows [B Lpad][576]][rotated q^R [B s][H][64]][K^C [B Lpad][H][128]][V^C [B
+// Lpad][H][128]]
 struct PfWs {
-    size_t off_rows, off_qr, off_kc, off_vc, total;
+    size_t off_max, off_rows, off_qr, off_kc, off_vc, total;
     long long lpad;   // max_seq_len rounded up to 128 rows (which may pass 2^31)
 };
 
@@ -240,7 +241,8 @@ PfWs pf_ws(int H, int B, int s, int max_seq_len)
     PfWs w;
     w.lpad = ((long long)max_seq_len + 127) / 128 * 128;
     const size_t rows = (size_t)B * w.lpad;
-    w.off_rows = kWsAlign;
+    w.off_max = 32;
+    w.off_rows = align_up(w.off_max + ((size_t)B + H) * sizeof(uint32_t), kWsAlign);
     w.off_qr = align_up(w.off_rows + rows * kRow * 2, kWsAlign);
     w.off_kc = align_up(w.off_qr + (size_t)B * s * H * kDr * 2, kWsAlign);
     w.off_vc = align_up(w.off_kc + rows * H * kDh * 2, kWsAlign);
@@ -468,7 +470,7 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
     const int lpad = (int)w.lpad, M = (int)(B * w.lpad);
     if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
     char *ws = (char *)workspace;
-    uint32_t *err = (uint32_t *)ws, *max_bits = err + 2;
+    uint32_t *err = (uint32_t *)ws, *max_bits = (uint32_t *)(ws + w.off_max);
     bf16 *rows = (bf16 *)(ws + w.off_rows), *q_rot = (bf16 *)(ws + w.off_qr);
     bf16 *kc = (bf16 *)(ws + w.off_kc), *vc = (bf16 *)(ws + w.off_vc);
     const long long cap_blocks = (long long)max_blocks * kBlock;
@@ -506,7 +508,8 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
         pm.kc = mkc;
         pm.vc = mvc;
     }
-    if (cudaMemsetAsync(err, 0, 8 * sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
+    if (cudaMemsetAsync(ws, 0, w.off_max + (kHalfV ? ((size_t)B + H) * sizeof(uint32_t) : 0), strm) != cudaSuccess)
+        return MLA_ERR_CUDA;
     const PrepareBlocks pb(B, lpad, s, H, kHalfV);
     prefill_prepare_kernel<Rows, kHalfV><<<pb.rows + pb.rope + pb.weights, 256, 0, strm>>>(
         cache, pb, num_blocks, block_table, max_blocks, seq_lens, s, H, lpad, l_cap, rows, (const bf16 *)q_rope, q_pos,
@@ -518,7 +521,7 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
     // one's start and epilogue with the other's products (73 us a product against 98
     // at 4,096 rows x 128 heads); fewer: four, which hide a lone CTA's loads (9.4
     // against 11.1 us at 1,152 rows x 16 heads).
-    const TcEpiTmaStorePair epi{kHalfV ? max_bits : nullptr};
+    const TcEpiTmaStorePair epi{kHalfV ? max_bits : nullptr, max_bits + B, lpad};
     const cudaError_t ge =
         2ll * ((M + 127) / 128) * ((H * kDh + 255) / 256) > sm_count()
             ? launch_tc_gemm<256, false, TcEpiTmaStorePair, false, 2, true>(ma, muk, M, H * kDh, kDc, 1, epi, err, strm,
@@ -535,7 +538,8 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
     pa.scale_log2 = softmax_scale(dims) * kLog2e;
     pa.out_lse = out_lse;
     pa.err = err;
-    pa.max_bits = max_bits;
+    pa.max_lat = max_bits;
+    pa.max_w = max_bits + B;
     pa.counter = (int *)(err + 4);
     pa.qtiles = (s + 127) / 128;
     pa.items = pa.qtiles * H * B;

@@ -33,13 +33,13 @@ struct GemmSmem {
     static constexpr int TMEM_COLS = BN <= 32 ? 32 : (BN <= 64 ? 64 : (BN <= 128 ? 128 : 256));
 };
 
-// 2^n, |n| <= 126, and the exponent e of TcEpiTmaStorePair: a pattern with
-// exponent field x stands for less than 2^(x - 126), so the bound is
-// 2^(9 + x - 126 + y - 126).
+// 2^n, |n| <= 126, and the exponent e of TcEpiTmaStorePair for two largest
+// magnitudes' patterns: one with exponent field x stands for less than 2^(x - 126),
+// so the bound is 2^(9 + x - 126 + y - 126).
 __device__ __forceinline__ float exp2_int(int n) { return __uint_as_float((uint32_t)(127 + n) << 23); }
-__device__ __forceinline__ int half_exponent(const uint32_t *max_bits)
+__device__ __forceinline__ int half_exponent(const uint32_t *a, const uint32_t *b)
 {
-    const int e = (int)(__ldcg(max_bits) >> 7) + (int)(__ldcg(max_bits + 1) >> 7) - 258;
+    const int e = (int)(__ldcg(a) >> 7) + (int)(__ldcg(b) >> 7) - 258;
     return min(max(e, -126), 126);
 }
 
@@ -157,9 +157,12 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
             // [128 rows][128 B] (128-byte swizzle), stored with TMA by one
             // thread: whole lines rather than 32 rows' pieces per instruction
             const int r = q * 32 + lane;
-            const float f = epi.factor(second);
+            // (a factor holds for 128 columns and, where there is one, 128 rows of A)
+            float f = epi.factor(second, m0, n0);
+            const float f1 = BN > 128 ? epi.factor(second, m0, n0 + 128) : f;
 #pragma unroll 1
             for (int c = 0; c < BN; c += 32) {
+                if (c == 128) f = f1;
                 uint32_t v[32];
                 if (ok) {
                     sm100::tmem_ld16(sm100::tmem_addr(tmem, q * 32, c), v);
@@ -225,21 +228,26 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
 struct TcEpiTmaStore {
     static constexpr bool kStaged = true;
     int split_n = 0;
-    __device__ float factor(bool) const { return 0.f; }
+    __device__ float factor(bool, int, int) const { return 0.f; }
     __device__ uint32_t pack(float lo, float hi, float) const { return pack_bf162(lo, hi); }
     __device__ void operator()(int, int, int, const float *) const {}
 };
 
-// The same for a pair of products, the second's outputs (where max_bits is given)
-// f16 scaled by 2^-e, for operands whose largest finite magnitudes' bf16 patterns
-// are max_bits[0] and max_bits[1]: with K = 512 no product is beyond 2^9 times
-// both, and e (half_exponent) is the least that keeps that bound at 2^15.
+// The same for a pair of products, the second's outputs (where max_a is given) f16
+// scaled by 2^-e.  A is cut into blocks of `rows` rows (a multiple of 128) and B into
+// 128 columns, and max_a[] and max_b[] hold the bf16 patterns of each block's largest
+// finite magnitude: with K = 512 no product is beyond 2^9 times both, and e
+// (half_exponent) is the least that keeps that bound at 2^15.
 struct TcEpiTmaStorePair {
     static constexpr bool kStaged = true;
-    const uint32_t *max_bits;
+    const uint32_t *max_a, *max_b;
+    int rows;
     int split_n = 0;
     // (0: bf16)
-    __device__ float factor(bool second) const { return second && max_bits ? exp2_int(-half_exponent(max_bits)) : 0.f; }
+    __device__ float factor(bool second, int m, int n) const
+    {
+        return second && max_a ? exp2_int(-half_exponent(max_a + m / rows, max_b + n / 128)) : 0.f;
+    }
     __device__ uint32_t pack(float lo, float hi, float f) const
     {
         return f != 0.f ? pack_half2(lo * f, hi * f) : pack_bf162(lo, hi);

@@ -55,11 +55,11 @@
 // latents there are read exactly, and the two roundings to 8 bits of P and V^C
 // would be two thirds of the output's squared error (its relative rms 0.0029, so
 // 0.0021, of which the output's own rounding to bf16 is 0.0017; the rest is the
-// rounding of K^C and the queries).  f16 needs its range kept: V^C
-// is stored times 2^-e, with e from the largest latent and weight magnitudes
-// (prefill_prepare_kernel), so that none overflows whatever the weights, and P
-// is formed as 2^7 p (p <= 2^8), which leaves weights down to 2^-21 their 11
-// bits.  Both factors are powers of two and come off in the epilogue.
+// rounding of K^C and the queries).  f16 needs its range kept: V^C is stored times
+// 2^-e, with an e of each sequence and head from its largest latent and weight
+// magnitudes (prefill_prepare_kernel), so that none overflows whatever the weights,
+// and a sequence's outputs do not depend on the others of its batch.  P is formed as
+// 2^7 p (p <= 2^8), which leaves weights down to 2^-21 their 11 bits.  Both factors are powers of two and come off in the epilogue.
 #pragma once
 
 #include <type_traits>
@@ -105,7 +105,7 @@ struct PrefillArgs {
     float scale_log2;
     float *out_lse;               // [B][s][H] or null
     uint32_t *err;
-    const uint32_t *max_bits;     // kHalfV: largest magnitudes of the latents and of U^V (bf16 patterns)
+    const uint32_t *max_lat, *max_w;   // kHalfV: largest magnitudes (bf16 patterns) of a sequence's latents, a head's U^V
     unsigned long long limit_ns;
 };
 
@@ -470,7 +470,7 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
                 sm100::tc_fence_after();
             }
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-            const float vf = kHalfV ? exp2_int(half_exponent(a.max_bits)) : 1.f;
+            const float vf = kHalfV ? exp2_int(half_exponent(a.max_lat + it.b, a.max_w + it.head)) : 1.f;
             auto o_of = [&](uint32_t x) { return kHalfV ? __uint_as_float(x) * inv * vf : __uint_as_float(x) * inv; };
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
@@ -534,21 +534,25 @@ __device__ __forceinline__ uint32_t finite_max(uint4 v)
 //     the sequence's length, and every row of an invalid sequence, are zero);
 //   - the chunk's RoPE queries rotated to q_pos (copied when q_pos is null), a
 //     warp taking one token's 32 pairs of up to 16 heads;
-//   - kHalfV: the largest finite magnitudes, as bf16 patterns, of the gathered
-//     latents and of the weights w_uv (maxima, which no order of the atomics
-//     changes).
+//   - kHalfV: the largest finite magnitudes, as bf16 patterns, of each sequence's
+//     gathered latents (max_bits[b]) and of each head's weights w_uv (max_bits[B + i]):
+//     maxima, which no order of the atomics changes.  A CTA's rows are one sequence's
+//     (lpad is a multiple of 128, and 128 rows are 36 CTAs) and its weights one head's
+//     (8 CTAs each).
 // Every thread has one piece of work: phases one after the other in each thread
 // left the memory waiting for the angles.  Rows: how the cache's rows are read as
 // bf16 (Bf16Rows, Int4Rows).
 struct PrepareBlocks {
     long long row_units, rope_units, w_units;   // 16-byte units; (token, heads, pair); 16-byte units
     unsigned rows, rope, weights;               // CTAs
+    int B;
     PrepareBlocks(int B, int lpad, int s, int H, bool half_v)
         : row_units((long long)B * lpad * (kRow / 8)),
           rope_units((long long)B * s * ((H + kPfRopeHeads - 1) / kPfRopeHeads) * (kDr / 2)),
           w_units(half_v ? (long long)H * kDh * kDc / 8 : 0), rows((unsigned)((row_units + 255) / 256)),
-          rope((unsigned)((rope_units + 255) / 256)), weights((unsigned)((w_units + 1023) / 1024))
+          rope((unsigned)((rope_units + 255) / 256)), weights((unsigned)((w_units + 1023) / 1024)), B(B)
     {
+        static_assert(128 * (kRow / 8) % 256 == 0 && kDh * kDc / 8 % 1024 == 0, "a CTA's maximum has one owner");
     }
 };
 
@@ -607,7 +611,11 @@ prefill_prepare_kernel(const Rows cache, const PrepareBlocks blocks, int num_blo
         most = __reduce_max_sync(0xffffffffu, max(most & 0xFFFFu, most >> 16));
         if ((threadIdx.x & 31) == 0) atomicMax(&cta_max, most);
         __syncthreads();
-        if (threadIdx.x == 0) atomicMax(max_bits + (weights ? 1 : 0), cta_max);
+        if (threadIdx.x == 0) {
+            const int owner = weights ? blocks.B + (int)((cta - blocks.rows - blocks.rope) / (kDh * kDc / 8 / 1024))
+                                      : (int)(cta * 256ll / (kRow / 8) / lpad);
+            atomicMax(max_bits + owner, cta_max);
+        }
     }
 }
 

@@ -427,8 +427,10 @@ mla_status_t mla_decode_int4(const mla_dims_t *dims, const void *q_abs, const vo
  * the rows the cache stands for (the chunk's own rows included: append them
  * first).  Arguments, workspace (mla_prefill_workspace_size), outputs, errors and
  * size limits as for mla_prefill, with `codes` and `scales` in place of `cache`, and
- * max_blocks * block_size below 2^31 (MLA_ERR_UNSUPPORTED).  v^C and the softmax weights are rounded to f16 (under a
- * power of two that keeps v^C in range) where mla_prefill rounds them to bf16.
+ * max_blocks * block_size below 2^31 (MLA_ERR_UNSUPPORTED).  v^C and the softmax weights are rounded to f16 (v^C
+ * under a power of two that keeps it in range, of its sequence's largest latent c and
+ * its head's largest weight w: values down to 2^-27 times 512 c w keep 11 bits) where
+ * mla_prefill rounds them to bf16.
  */
 mla_status_t mla_prefill_int4(const mla_dims_t *dims, const void *q_nope, const void *q_rope,
                               const int32_t *q_pos, const void *w_uk, const void *w_uv,
