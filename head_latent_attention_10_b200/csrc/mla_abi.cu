@@ -744,6 +744,7 @@ mla_status_t mla_decode(const mla_dims_t *dims, const void *q_abs, const void *c
     if (!q_abs || !cache || !block_table || !seq_lens || !out_latent) return MLA_ERR_INVALID_ARG;
     if (!aligned16(q_abs) || !aligned16(cache) || !aligned16(out_latent)) return MLA_ERR_INVALID_ARG;
     if (!workspace) return MLA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
     cudaStream_t strm = as_stream(stream);
     char *ws = (char *)workspace;
     uint32_t *err = (uint32_t *)ws;
@@ -856,6 +857,7 @@ mla_status_t mla_prefill(const mla_dims_t *dims, const void *q_nope, const void 
         return MLA_ERR_INVALID_ARG;
     if (!prefill_sizes_ok(B, s, dims->num_heads, max_seq_len)) return MLA_ERR_UNSUPPORTED;
     if (!workspace) return MLA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
     return run_prefill<false>(dims, q_nope, q_rope, q_pos, w_uk, w_uv, Bf16Rows{(const bf16 *)cache}, num_blocks, block_table,
                        max_blocks, seq_lens, B, s, max_seq_len, out, out_lse, workspace, ws_bytes, flags,
                        as_stream(stream));
@@ -898,6 +900,7 @@ mla_status_t mla_decode_fp8(const mla_dims_t *dims, const void *q_abs, const voi
     if (!aligned16(q_abs) || !aligned16(codes) || !aligned16(scales) || !aligned16(out_latent))
         return MLA_ERR_INVALID_ARG;
     if (!workspace) return MLA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
     cudaStream_t strm = as_stream(stream);
     char *ws = (char *)workspace;
     const mla_status_t r = run_tc_decode<true>(dims, q_abs, codes, scales, num_blocks, block_table, max_blocks,
@@ -967,6 +970,7 @@ mla_status_t mla_decode_int4(const mla_dims_t *dims, const void *q_abs, const vo
         return MLA_ERR_INVALID_ARG;
     if (!int4_sizes_ok(B, s, dims->num_heads, max_blocks)) return MLA_ERR_UNSUPPORTED;
     if (!workspace) return MLA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
     cudaStream_t strm = as_stream(stream);
     char *ws = (char *)workspace;
     const mla_status_t r =
@@ -1005,6 +1009,7 @@ mla_status_t mla_prefill_int4(const mla_dims_t *dims, const void *q_nope, const 
     if (!int4_sizes_ok(B, s, dims->num_heads, max_blocks) || !prefill_sizes_ok(B, s, dims->num_heads, max_seq_len))
         return MLA_ERR_UNSUPPORTED;
     if (!workspace) return MLA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
     return run_prefill<true>(dims, q_nope, q_rope, q_pos, w_uk, w_uv,
                        Int4Rows{(const uint8_t *)codes, (const uint8_t *)scales}, num_blocks, block_table, max_blocks,
                        seq_lens, B, s, max_seq_len, out, out_lse, workspace, ws_bytes, flags, as_stream(stream));

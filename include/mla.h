@@ -200,8 +200,8 @@ size_t mla_decode_workspace_size(const mla_dims_t *dims, int B, int s, int max_s
  *   out_lse     [B*s][H] fp32 natural-log softmax denominator of the scaled
  *               logits, or NULL.  A query with no visible key gets a zero
  *               latent and lse = -inf (and MLA_DEVERR_SEQ_LEN).
- *   workspace   device buffer of ws_bytes >= mla_decode_workspace_size();
- *               its first 4 bytes are the device error word (cleared by the
+ *   workspace   device buffer of ws_bytes >= mla_decode_workspace_size(),
+ *               16-byte aligned; its first 4 bytes are the device error word (cleared by the
  *               call); the rest holds the split plan and partial results.
  *   flags       MLA_SYNC_CHECK, MLA_FORCE_SIMPLE (MLA_DEBUG_STALL,
  *               MLA_DEBUG_COMBINE_ALL: tests only).
@@ -300,10 +300,10 @@ size_t mla_prefill_workspace_size(const mla_dims_t *dims, int B, int s, int max_
  *               B * round_up(max_seq_len, 128) latent rows per head
  *   out         [B*s][H][d_head] bf16 (per-head outputs, O not applied)
  *   out_lse     [B*s][H] fp32 natural-log softmax denominator, or NULL
- *   workspace   ws_bytes >= mla_prefill_workspace_size(); its first 4 bytes
- *               are the device error word (cleared by the call, read with
- *               mla_decode_error); the rest holds the gathered latents, the
- *               rotated q^R and the expanded K^C and V^C.
+ *   workspace   ws_bytes >= mla_prefill_workspace_size(), 16-byte aligned; its
+ *               first 4 bytes are the device error word (cleared by the call,
+ *               read with mla_decode_error); the rest holds the gathered
+ *               latents, the rotated q^R and the expanded K^C and V^C.
  *   flags       MLA_SYNC_CHECK
  * A sequence with seq_lens[b] < s, > max_seq_len or > max_blocks * 64 gets
  * zero outputs, lse = -inf and MLA_DEVERR_SEQ_LEN.  B = 0 is a no-op; with
