@@ -968,7 +968,10 @@ mla_status_t mla_decode_int4(const mla_dims_t *dims, const void *q_abs, const vo
     if (!q_abs || !codes || !scales || !block_table || !seq_lens || !out_latent) return MLA_ERR_INVALID_ARG;
     if (!aligned16(q_abs) || !aligned16(codes) || !aligned16(scales) || !aligned16(out_latent))
         return MLA_ERR_INVALID_ARG;
-    if (!int4_sizes_ok(B, s, dims->num_heads, max_blocks)) return MLA_ERR_UNSUPPORTED;
+    // the plan's sums over the sequences, and its last range's end, are 32-bit as well
+    if (!int4_sizes_ok(B, s, dims->num_heads, max_blocks) ||
+        (long long)B * (max_blocks + kSwitchTiles) + kMaxRanges > (1ll << 31) - 1)
+        return MLA_ERR_UNSUPPORTED;
     if (!workspace) return MLA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MLA_ERR_INVALID_ARG;
     cudaStream_t strm = as_stream(stream);

@@ -413,8 +413,9 @@ mla_status_t mla_gather_latent_int4(const mla_dims_t *dims, const void *codes, c
  * mla_decode_int4 -- mla_decode over the 4-bit cache: the same attention on the
  * rows the cache stands for (bf16 operands, fp32 accumulation).  Arguments, flags,
  * workspace (mla_decode_workspace_size), outputs and errors as for mla_decode,
- * with `codes` and `scales` in place of `cache`.  B * s * num_heads and
- * max_blocks * block_size must be below 2^31 (MLA_ERR_UNSUPPORTED).
+ * with `codes` and `scales` in place of `cache`.  B * s * num_heads,
+ * max_blocks * block_size and B * (max_blocks + 4) + 148 must be below 2^31
+ * (MLA_ERR_UNSUPPORTED).
  */
 mla_status_t mla_decode_int4(const mla_dims_t *dims, const void *q_abs, const void *codes,
                              const void *scales, int num_blocks, const int32_t *block_table,
