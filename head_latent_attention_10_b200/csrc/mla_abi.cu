@@ -427,6 +427,7 @@ mla_status_t run_simple_decode(const mla_dims_t *dims, const void *q_abs, const 
 {
     const int H = dims->num_heads, T = B * s;
     uint32_t *err = (uint32_t *)ws;
+    if ((long long)max_blocks * kBlock > 65535ll * kSimpleSplit) return MLA_ERR_UNSUPPORTED;   // splits: the grid's z
     const SimpleWs w = simple_ws(H, T, max_blocks * kBlock);
     if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
     if (cudaMemsetAsync(err, 0, sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;

@@ -207,7 +207,8 @@ size_t mla_decode_workspace_size(const mla_dims_t *dims, int B, int s, int max_s
  *               MLA_DEBUG_COMBINE_ALL: tests only).
  * Sequences are independent; calls that share a workspace must not overlap
  * on the GPU.  B = 0 is a no-op.  With B > 0, num_blocks and max_blocks must
- * be at least 1 (MLA_ERR_INVALID_ARG otherwise).
+ * be at least 1 (MLA_ERR_INVALID_ARG otherwise); with MLA_FORCE_SIMPLE,
+ * max_blocks is at most 1,048,560 (MLA_ERR_UNSUPPORTED).
  */
 mla_status_t mla_decode(const mla_dims_t *dims, const void *q_abs, const void *cache,
                         int num_blocks, const int32_t *block_table, int max_blocks,

@@ -34,3 +34,12 @@ def test_tiles_of_the_batch_are_counted_in_32_bits(M):
         assert B * (mb + 4) + 148 > TOP and decode(M, B=B, mb=mb) == M.MLA_ERR_UNSUPPORTED, (B, mb)
     for B, mb in ((63, (1 << 25) - 1), (1 << 16, (1 << 15) - 5), (1 << 26, 27)):
         assert B * (mb + 4) + 148 <= TOP and decode(M, B=B, mb=mb) != M.MLA_ERR_UNSUPPORTED, (B, mb)
+
+
+@pytest.mark.parametrize("name", ["mla_decode", "mla_decode_int4"])
+def test_splits_of_the_cuda_core_decode_are_limited(M, name):
+    """A split is 1,024 tokens, and splits are its grid's third dimension."""
+    most = 65535 * 1024 // 64
+    assert decode(M, mb=most + 1, flags=M.MLA_FORCE_SIMPLE, name=name) == M.MLA_ERR_UNSUPPORTED
+    assert decode(M, mb=most, flags=M.MLA_FORCE_SIMPLE, name=name) != M.MLA_ERR_UNSUPPORTED
+    assert decode(M, mb=most + 1, name=name) != M.MLA_ERR_UNSUPPORTED
