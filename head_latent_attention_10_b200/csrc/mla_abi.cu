@@ -86,6 +86,15 @@ RopeTable rope_table(const mla_dims_t *d)
 
 inline mla_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
+// Whether a runtime call failed.  The runtime keeps its error until it is read: read
+// here, or the next call that checks a launch would report it as its own.
+inline bool failed(cudaError_t e)
+{
+    if (e == cudaSuccess) return false;
+    cudaGetLastError();
+    return true;
+}
+
 // Bound of every device-side wait (ns).  With MLA_DEBUG_STALL (a test hook
 // for failure detection) waits give up after 20 ms instead.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
@@ -100,7 +109,7 @@ constexpr int kMaxDevices = 64;
 inline int current_device()
 {
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
+    if (failed(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) return -1;
     return dev;
 }
 
@@ -115,7 +124,7 @@ cudaError_t ensure_smem_attr(K kern, int bytes, std::atomic<bool> *done)
     std::lock_guard<std::mutex> g(g_dev_mu);
     if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    if (!failed(e)) done[dev].store(true, std::memory_order_release);
     return e;
 }
 
@@ -131,10 +140,7 @@ void *symbol_address(const T &sym, std::atomic<void *> *addr)
     std::lock_guard<std::mutex> g(g_dev_mu);
     p = addr[dev].load(std::memory_order_relaxed);
     if (p) return p;
-    if (cudaGetSymbolAddress(&p, sym) != cudaSuccess) {
-        cudaGetLastError();
-        return nullptr;
-    }
+    if (failed(cudaGetSymbolAddress(&p, sym))) return nullptr;
     addr[dev].store(p, std::memory_order_release);
     return p;
 }
@@ -164,7 +170,9 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    failed(e);
+    return e;
 }
 
 // C = A B on tcgen05; `c` is the output tensor map of the staged (TMA store)
@@ -257,7 +265,7 @@ int sm_count()
     if (dev < 0) return 0;
     int sms = sms_cache[dev].load(std::memory_order_acquire);
     if (sms <= 0) {
-        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 0;
+        if (failed(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) || sms <= 0) return 0;
         sms_cache[dev].store(sms, std::memory_order_release);
     }
     return sms;
@@ -303,7 +311,7 @@ mla_status_t run_tc_decode(const mla_dims_t *dims, const void *q_abs, const void
         if (!tmap(&mkv, cache, kRow, (uint64_t)num_blocks * kBlock, 1, kRow, 0, 64, kT64)) return MLA_ERR_CUDA;
     }
     // the error word, the plan and the merge flags
-    if (cudaMemsetAsync(ws, 0, w.off_zero_end, strm) != cudaSuccess) return MLA_ERR_CUDA;
+    if (failed(cudaMemsetAsync(ws, 0, w.off_zero_end, strm))) return MLA_ERR_CUDA;
     int32_t *plan = (int32_t *)(ws + w.off_plan);
     DecArgs da;
     da.flags = (int *)(ws + w.off_flags);
@@ -430,7 +438,7 @@ mla_status_t run_simple_decode(const mla_dims_t *dims, const void *q_abs, const 
     if ((long long)max_blocks * kBlock > 65535ll * kSimpleSplit) return MLA_ERR_UNSUPPORTED;   // splits: the grid's z
     const SimpleWs w = simple_ws(H, T, max_blocks * kBlock);
     if (ws_bytes < w.total) return MLA_ERR_WORKSPACE;
-    if (cudaMemsetAsync(err, 0, sizeof(uint32_t), strm) != cudaSuccess) return MLA_ERR_CUDA;
+    if (failed(cudaMemsetAsync(err, 0, sizeof(uint32_t), strm))) return MLA_ERR_CUDA;
     float *po = (float *)(ws + w.off_o);
     float *pl = (float *)(ws + w.off_lse);
     dim3 grid(T, H / kSimpleHeads, w.nsplit);
@@ -509,7 +517,7 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
         pm.kc = mkc;
         pm.vc = mvc;
     }
-    if (cudaMemsetAsync(ws, 0, w.off_max + (kHalfV ? ((size_t)B + H) * sizeof(uint32_t) : 0), strm) != cudaSuccess)
+    if (failed(cudaMemsetAsync(ws, 0, w.off_max + (kHalfV ? ((size_t)B + H) * sizeof(uint32_t) : 0), strm)))
         return MLA_ERR_CUDA;
     const PrepareBlocks pb(B, lpad, s, H, kHalfV);
     prefill_prepare_kernel<Rows, kHalfV><<<pb.rows + pb.rope + pb.weights, 256, 0, strm>>>(
@@ -555,8 +563,8 @@ mla_status_t run_prefill(const mla_dims_t *dims, const void *q_nope, const void 
     if (ae != cudaSuccess) return MLA_ERR_CUDA;
     if (flags & MLA_SYNC_CHECK) {
         uint32_t h = 0;
-        if (cudaMemcpyAsync(&h, err, sizeof h, cudaMemcpyDeviceToHost, strm) != cudaSuccess ||
-            cudaStreamSynchronize(strm) != cudaSuccess)
+        if (failed(cudaMemcpyAsync(&h, err, sizeof h, cudaMemcpyDeviceToHost, strm)) ||
+            failed(cudaStreamSynchronize(strm)))
             return MLA_ERR_CUDA;
         if (h) return MLA_ERR_DEVICE;
     }
@@ -760,9 +768,9 @@ mla_status_t mla_decode(const mla_dims_t *dims, const void *q_abs, const void *c
     }
     if (flags & MLA_SYNC_CHECK) {
         uint32_t host = 0;
-        if (cudaMemcpyAsync(&host, err, sizeof host, cudaMemcpyDeviceToHost, strm) != cudaSuccess)
+        if (failed(cudaMemcpyAsync(&host, err, sizeof host, cudaMemcpyDeviceToHost, strm)))
             return MLA_ERR_CUDA;
-        if (cudaStreamSynchronize(strm) != cudaSuccess) return MLA_ERR_CUDA;
+        if (failed(cudaStreamSynchronize(strm))) return MLA_ERR_CUDA;
         if (host) return MLA_ERR_DEVICE;
     }
     return MLA_OK;
@@ -791,10 +799,10 @@ mla_status_t mla_decode_error(const void *workspace, uint32_t *err_host, int cle
 {
     if (!workspace || !err_host) return MLA_ERR_INVALID_ARG;
     cudaStream_t s = as_stream(stream);
-    if (cudaMemcpyAsync(err_host, workspace, sizeof(uint32_t), cudaMemcpyDeviceToHost, s) != cudaSuccess)
+    if (failed(cudaMemcpyAsync(err_host, workspace, sizeof(uint32_t), cudaMemcpyDeviceToHost, s)))
         return MLA_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return MLA_ERR_CUDA;
-    if (clear && cudaMemsetAsync((void *)workspace, 0, sizeof(uint32_t), s) != cudaSuccess)
+    if (failed(cudaStreamSynchronize(s))) return MLA_ERR_CUDA;
+    if (clear && failed(cudaMemsetAsync((void *)workspace, 0, sizeof(uint32_t), s)))
         return MLA_ERR_CUDA;
     return MLA_OK;
 }
@@ -909,8 +917,8 @@ mla_status_t mla_decode_fp8(const mla_dims_t *dims, const void *q_abs, const voi
     if (r != MLA_OK) return r;
     if (flags & MLA_SYNC_CHECK) {
         uint32_t host = 0;
-        if (cudaMemcpyAsync(&host, ws, sizeof host, cudaMemcpyDeviceToHost, strm) != cudaSuccess ||
-            cudaStreamSynchronize(strm) != cudaSuccess)
+        if (failed(cudaMemcpyAsync(&host, ws, sizeof host, cudaMemcpyDeviceToHost, strm)) ||
+            failed(cudaStreamSynchronize(strm)))
             return MLA_ERR_CUDA;
         if (host) return MLA_ERR_DEVICE;
     }
@@ -986,8 +994,8 @@ mla_status_t mla_decode_int4(const mla_dims_t *dims, const void *q_abs, const vo
     if (r != MLA_OK) return r;
     if (flags & MLA_SYNC_CHECK) {
         uint32_t host = 0;
-        if (cudaMemcpyAsync(&host, ws, sizeof host, cudaMemcpyDeviceToHost, strm) != cudaSuccess ||
-            cudaStreamSynchronize(strm) != cudaSuccess)
+        if (failed(cudaMemcpyAsync(&host, ws, sizeof host, cudaMemcpyDeviceToHost, strm)) ||
+            failed(cudaStreamSynchronize(strm)))
             return MLA_ERR_CUDA;
         if (host) return MLA_ERR_DEVICE;
     }

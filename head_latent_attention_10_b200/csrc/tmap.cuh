@@ -27,6 +27,8 @@ inline EncodeTiledFn encode_fn()
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<EncodeTiledFn>(p);
+        else
+            cudaGetLastError();   // (an error left behind would be the next launch's)
     });
     return fn;
 }
