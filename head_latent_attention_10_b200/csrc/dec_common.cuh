@@ -191,7 +191,7 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
 __host__ __device__ inline int plan_list_off(int B) { return (B + 9) & ~3; }   // 16-byte aligned, after plan[5 + B]
 __host__ __device__ inline int plan_ints(int B) { return plan_list_off(B) + 4 * B; }
 
-// `work` (with `publish`): raised by the number of listed sequences the
+// `work` (with `publish`, or null): raised by the number of listed sequences the
 // decode kernel does not merge itself (empty ones, those cut into three or
 // more pieces, and with !merge_two the two-piece ones too).
 __device__ void plan_range(const int32_t *seq_lens, int B, int s, int max_blocks, int ranges, int rng, bool publish,
@@ -270,7 +270,7 @@ __device__ void plan_range(const int32_t *seq_lens, int B, int s, int max_blocks
             }
             run_v += t > 0 ? t + kSwitchTiles : 0;
         }
-        if (left) atomicAdd(work, left);
+        if (work && left) atomicAdd(work, left);
         int ci = cnt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {

@@ -214,7 +214,8 @@ SimpleWs simple_ws(int H, int T, int max_seq_len)
 
 // Tensor-core decode workspace: [error word][plan][partial latents][partial lse2]
 // [merge flags][partial latents][partial lse2]; the first off_zero_end bytes
-// are zeroed per call
+// are zeroed per call (of the 4-bit decode, which merges in its combine alone: the
+// error word)
 struct TcWs {
     size_t off_plan, off_flags, off_zero_end, off_o, off_lse, total;
 };
@@ -379,14 +380,9 @@ mla_status_t run_int4_decode(const mla_dims_t *dims, const void *q_abs, const vo
     if (ensure_smem_attr(tc_decode_int4_kernel, kD4Smem, attr4) != cudaSuccess) return MLA_ERR_CUDA;
     const int groups = dec_groups(H, s), ranges = decode_int4_ranges(groups, B, max_blocks);
     if (ranges <= 0) return MLA_ERR_CUDA;
-    // the error word, the plan and its count
-    const long long words = w.off_zero_end / 4, most_clear = sm_count();
-    cudaError_t e = launch_pdl(dec4_clear_kernel,
-                               dim3((unsigned)(words / 1024 < most_clear ? words / 1024 + 1 : most_clear)), dim3(256), 0,
-                               strm, (int *)ws, words);
+    cudaError_t e = launch_pdl(dec4_clear_kernel, dim3(1), dim3(32), 0, strm, (uint32_t *)ws);
     count_launch();
     if (e != cudaSuccess) return MLA_ERR_CUDA;
-    int *cflags = (int *)(ws + w.off_flags);
     Dec4Args da;
     da.q_abs = (const bf16 *)q_abs;
     da.codes = (const uint8_t *)codes;
@@ -394,7 +390,6 @@ mla_status_t run_int4_decode(const mla_dims_t *dims, const void *q_abs, const vo
     da.block_table = block_table;
     da.seq_lens = seq_lens;
     da.plan = (int32_t *)(ws + w.off_plan);
-    da.work = cflags + 2 * (size_t)B * groups * 4;
     da.out = (bf16 *)out_latent;
     da.out_lse = out_lse;
     da.part_o = (float *)(ws + w.off_o);

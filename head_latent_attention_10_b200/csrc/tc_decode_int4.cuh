@@ -82,7 +82,6 @@ struct Dec4Args {
     const uint8_t *codes, *scales;    // [num_blocks][64][288], [num_blocks][64][36]
     const int32_t *block_table, *seq_lens;
     int32_t *plan;                    // written by CTA 0 for the combine
-    int *work;                        // (plan_range counts the sequences to merge here)
     bf16 *out;
     float *out_lse;
     float *part_o, *part_lse2;        // [2*ranges][s*H][512], [2*ranges][s*H]
@@ -118,14 +117,14 @@ __device__ __noinline__ uint64_t d4_wait_tick(uint64_t t0, volatile int *abort, 
     return t0;
 }
 
-// The call's error word, plan and counts cleared.  A kernel rather than a memset,
-// because a memset ends before the next kernel is launched: here the decode's set-up
-// overlaps it.
-__global__ void __launch_bounds__(256) dec4_clear_kernel(int *p, long long n)
+// The call's error word cleared (the plan is written whole by plan_range).  A kernel
+// rather than a memset, because a memset ends before the next kernel is launched: here
+// the decode's set-up overlaps it.
+__global__ void __launch_bounds__(32) dec4_clear_kernel(uint32_t *err)
 {
     sm100::pdl_trigger();
     sm100::pdl_wait();
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) p[i] = 0;
+    if (threadIdx.x == 0) *err = 0;
 }
 
 #define D4_RARE(x) __builtin_expect(!!(x), 0)
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(kD4Threads, 1) tc_decode_int4_kernel(const Dec
     sm100::pdl_wait();
     if (warp == 2)
         plan_range(a.seq_lens, a.B, a.s, a.max_blocks, gridDim.x / a.groups, rng, blockIdx.x == 0, false, a.plan,
-                   a.work, a.err, rplan);
+                   nullptr, a.err, rplan);
     sm100::tc_fence_before();
     __syncthreads();
     sm100::tc_fence_after();
