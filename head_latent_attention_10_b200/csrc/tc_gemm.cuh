@@ -149,6 +149,13 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
     } else {
         // epilogue: warps 2..5 cover TMEM lane quarters 2,3,0,1
         const int q = warp & 3;
+        // (a factor holds for 128 columns and 128 rows of A; its loads pass while the
+        // products are formed)
+        float f = 0.f, f1 = 0.f;
+        if constexpr (Epi::kStaged) {
+            f = epi.factor(second, m0, n0);
+            f1 = BN > 128 ? epi.factor(second, m0, n0 + 128) : f;
+        }
         const bool ok = sm100::warp_wait(done, 0, abort_flag, err, limit_ns);
         sm100::tc_fence_after();
         const int m = m0 + q * 32 + lane;
@@ -157,9 +164,6 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
             // [128 rows][128 B] (128-byte swizzle), stored with TMA by one
             // thread: whole lines rather than 32 rows' pieces per instruction
             const int r = q * 32 + lane;
-            // (a factor holds for 128 columns and, where there is one, 128 rows of A)
-            float f = epi.factor(second, m0, n0);
-            const float f1 = BN > 128 ? epi.factor(second, m0, n0 + 128) : f;
 #pragma unroll 1
             for (int c = 0; c < BN; c += 32) {
                 if (c == 128) f = f1;

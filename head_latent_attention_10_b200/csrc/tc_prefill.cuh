@@ -566,6 +566,7 @@ prefill_prepare_kernel(const Rows cache, const PrepareBlocks blocks, int num_blo
 {
     unsigned cta = blockIdx.x;
     uint32_t most = 0;   // kHalfV: bf16 patterns of magnitudes, a pair
+    int owner = 0;       // and (of thread 0) whose they are
     const bool weights = cta >= blocks.rows + blocks.rope;
     if (cta < blocks.rows) {
         constexpr int kUnits = kRow / 8;                            // 16-byte units per row
@@ -575,6 +576,7 @@ prefill_prepare_kernel(const Rows cache, const PrepareBlocks blocks, int num_blo
             const int c = (int)(w % kUnits);
             const int b = (int)(row / lpad), j = (int)(row % lpad);
             const int L = seq_lens[b];
+            owner = b;
             const bool valid = prefill_valid(L, s, l_cap);
             if (!valid && j == 0 && c == 0) set_error(err, MLA_DEVERR_SEQ_LEN);
             uint4 v = make_uint4(0, 0, 0, 0);
@@ -599,7 +601,9 @@ prefill_prepare_kernel(const Rows cache, const PrepareBlocks blocks, int num_blo
         }
         return;
     } else {
-        const long long w = (cta - blocks.rows - blocks.rope) * 1024ll + threadIdx.x;
+        const unsigned wcta = cta - blocks.rows - blocks.rope;
+        const long long w = wcta * 1024ll + threadIdx.x;
+        owner = blocks.B + (int)(wcta / (kDh * kDc / 8 / 1024));
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (w + 256 * e < blocks.w_units) most = __vmaxu2(most, finite_max(w_uv[w + 256 * e]));
@@ -611,11 +615,7 @@ prefill_prepare_kernel(const Rows cache, const PrepareBlocks blocks, int num_blo
         most = __reduce_max_sync(0xffffffffu, max(most & 0xFFFFu, most >> 16));
         if ((threadIdx.x & 31) == 0) atomicMax(&cta_max, most);
         __syncthreads();
-        if (threadIdx.x == 0) {
-            const int owner = weights ? blocks.B + (int)((cta - blocks.rows - blocks.rope) / (kDh * kDc / 8 / 1024))
-                                      : (int)(cta * 256ll / (kRow / 8) / lpad);
-            atomicMax(max_bits + owner, cta_max);
-        }
+        if (threadIdx.x == 0) atomicMax(max_bits + owner, cta_max);
     }
 }
 
