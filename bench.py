@@ -67,6 +67,28 @@ def algorithmic_fp8(cfg: W.MLAConfig, seq_lens: np.ndarray, max_blocks: int):
     return byts - rows_read * D * 2 + rows_read * (D + 8), flops, rows_read
 
 
+def algorithmic_int4(cfg: W.MLAConfig, seq_lens: np.ndarray, max_blocks: int):
+    """As `algorithmic`, for the 4-bit cache: a cache row is 288 bytes of codes
+    plus 36 scale bytes (324 B/token)."""
+    byts, flops, rows_read = algorithmic(cfg, seq_lens, max_blocks)
+    D = cfg.d_c + cfg.d_r
+    return byts - rows_read * D * 2 + rows_read * (D // 2 + D // 16), flops, rows_read
+
+
+def int4_pages(M, rows):
+    """Codes and scales of pages [N][64][576] bf16, by the library's writer (which
+    turns the last 64 values of a row to its place in the N pages)."""
+    import torch
+    n = rows.shape[0]
+    codes = torch.empty(n, 64, 288, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(n, 64, 36, dtype=torch.uint8, device="cuda")
+    flat = rows.view(-1, 576)
+    pos = torch.arange(n * 64, dtype=torch.int32, device="cuda")
+    M.mla_append_latent_int4(M.dims(16), flat[:, :512].contiguous(), flat[:, 512:].contiguous(), torch.zeros_like(pos),
+                             pos, torch.arange(n, dtype=torch.int32, device="cuda")[None].contiguous(), codes, scales)
+    return codes, scales
+
+
 # DRAM bytes (read + write) the current decode kernel moves per cache token,
 # from one ncu capture (dram__bytes_read.sum + dram__bytes_write.sum) of
 # tc_decode64_kernel on the V2-shaped batch cut to 32 sequences (157.7 MB read
@@ -420,7 +442,7 @@ def run_ours(args):
 
 
 # ---------------------------------------------------- every config's decode
-def per_config(M, names, iters=30, fp8=False):
+def per_config(M, names, iters=30, fp8=False, int4=False):
     """The decode call (plan + decode + combine) on each named workload: its
     CUDA-event time on the launching stream (mean of `iters` back-to-back
     calls after 3 warm-ups), latent-cache GB/s, TFLOP/s and roofline
@@ -452,6 +474,9 @@ def per_config(M, names, iters=30, fp8=False):
             cache = None
         else:
             cache = torch.randn((nphys, cfg.block_size, D), generator=g, device="cuda").to(torch.bfloat16)
+            if int4:
+                codes, scales = int4_pages(M, cache)
+                cache = None
         q = torch.randn((cfg.T, cfg.H, D), generator=g, device="cuda")
         q[..., :cfg.d_c] *= 0.5
         q = q.to(torch.bfloat16)
@@ -466,6 +491,10 @@ def per_config(M, names, iters=30, fp8=False):
             call = lambda: M.mla_decode_fp8(dims, q, codes, scales, bt, slt, cfg.s, lat, lse, ws)
             byts, flops, rows = algorithmic_fp8(cfg, sl, table.shape[1])
             row_bytes = 584
+        elif int4:
+            call = lambda: M.mla_decode_int4(dims, q, codes, scales, bt, slt, cfg.s, lat, lse, ws)
+            byts, flops, rows = algorithmic_int4(cfg, sl, table.shape[1])
+            row_bytes = 324
         else:
             call = lambda: M.mla_decode(dims, q, cache, bt, slt, cfg.s, lat, lse, ws)
             byts, flops, rows = algorithmic(cfg, sl, table.shape[1])
@@ -490,7 +519,7 @@ def per_config(M, names, iters=30, fp8=False):
 
         t = timed(small)
         hbm_t, tc_t = byts / (pk["hbm"] * 1e9), flops / (pk["tc"] * 1e12)
-        r = {"workload": cfg.describe + (" (FP8 E4M3 cache)" if fp8 else ""), "us": t * 1e6,
+        r = {"workload": cfg.describe + (" (FP8 E4M3 cache)" if fp8 else " (4-bit cache)" if int4 else ""), "us": t * 1e6,
              "cache_gbs": rows * row_bytes / t / 1e9,
              "gbs": byts / t / 1e9, "tflops": flops / t / 1e12,
              "bound": "hbm" if hbm_t >= tc_t else "tensor", "roofline_us": max(hbm_t, tc_t) * 1e6,
@@ -525,7 +554,7 @@ def per_config(M, names, iters=30, fp8=False):
         del graph
         out[name] = r
         del cache, q, lat, lse, ws, bt, slt
-        if fp8:
+        if fp8 or int4:
             del codes, scales
         torch.cuda.empty_cache()
     return out
@@ -554,8 +583,9 @@ def prefill_flops(B, s, L, H, d_c=512, d_r=64, d_h=128):
     return att, exp_
 
 
-def prefill_bench(M, names=tuple(PREFILL_WORKLOADS), iters=10):
-    """mla_prefill on each workload: CUDA-event time of the whole call
+def prefill_bench(M, names=tuple(PREFILL_WORKLOADS), iters=10, int4=False):
+    """mla_prefill (int4: mla_prefill_int4, rows quantized by the library's writer) on
+    each workload: CUDA-event time of the whole call
     (gather + two expansion GEMMs + attention; mean of `iters` calls after 3
     warm-ups, each call preceded by a 256 MB L2 flush), its TFLOP/s and the
     fraction of the measured dense bf16 peak (the call is tensor-bound).
@@ -586,7 +616,12 @@ def prefill_bench(M, names=tuple(PREFILL_WORKLOADS), iters=10):
         o = torch.empty((B * s, H, 128), dtype=torch.bfloat16, device="cuda")
         lse = torch.empty((B * s, H), dtype=torch.float32, device="cuda")
         ws = torch.empty(M.mla_prefill_workspace_size(dims, B, s, L), dtype=torch.uint8, device="cuda")
-        call = lambda: M.mla_prefill(dims, q_nope, q_rope, q_pos, w_uk, w_uv, cache, bt, sl, s, L, o, lse, ws)
+        if int4:
+            codes, scales = int4_pages(M, cache)
+            call = lambda: M.mla_prefill_int4(dims, q_nope, q_rope, q_pos, w_uk, w_uv, codes, scales, bt, sl, s, L, o,
+                                              lse, ws)
+        else:
+            call = lambda: M.mla_prefill(dims, q_nope, q_rope, q_pos, w_uk, w_uv, cache, bt, sl, s, L, o, lse, ws)
         for _ in range(3):
             call()
         torch.cuda.synchronize()
@@ -771,6 +806,8 @@ def main():
     ap.add_argument("--prefill-only", action="store_true", help="time only the prefill workloads")
     ap.add_argument("--decode-only", default="", help="comma-separated workloads: time only their decode calls")
     ap.add_argument("--fp8", action="store_true", help="with --decode-only: the FP8-cache decode")
+    ap.add_argument("--int4", action="store_true", help="with --decode-only or --prefill-only: over the 4-bit cache as "
+                                                        "well, in the same process")
     ap.add_argument("--no-graph", action="store_true", help="launch the timed steps on the stream, not as a graph")
     ap.add_argument("--cpu-seconds", type=float, default=10.0)
     args = ap.parse_args()
@@ -784,13 +821,19 @@ def main():
         M.load_library()
         torch.cuda.set_device(int(os.environ.get("LOCAL_RANK", "0")))
         key = "per_config_fp8" if args.fp8 else "per_config"
-        print(json.dumps({key: per_config(M, args.decode_only.split(","), fp8=args.fp8)}), flush=True)
+        line = {key: per_config(M, args.decode_only.split(","), fp8=args.fp8)}
+        if args.int4:
+            line["per_config_int4"] = per_config(M, args.decode_only.split(","), int4=True)
+        print(json.dumps(line), flush=True)
     elif args.prefill_only:
         import torch
         import head_latent_attention_10_b200 as M
         M.load_library()
         torch.cuda.set_device(int(os.environ.get("LOCAL_RANK", "0")))
-        print(json.dumps({"prefill": prefill_bench(M), "folded_weights": fold_bench(M)}), flush=True)
+        line = {"prefill": prefill_bench(M), "folded_weights": fold_bench(M)}
+        if args.int4:
+            line["prefill_int4"] = prefill_bench(M, int4=True)
+        print(json.dumps(line), flush=True)
     else:
         run_ours(args)
 
