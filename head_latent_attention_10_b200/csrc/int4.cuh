@@ -46,7 +46,7 @@ __device__ __forceinline__ float int4_scale(uint32_t b) { return __uint_as_float
 // the constant kInt4CodeBits: 8 + x / s rounded to nearest-even, |x| <= 7.5 s; inv_s
 // is 1 / s in fp32.  x * inv_s is within 2^-24 of the quotient, relative.  With
 // x = X 2^a (X < 256) and s = S 2^b (8 <= S < 16), a quotient below 8 that is not a
-// tie k + 1/2 is at least 1/480 away from one, so the sum with 192, which the one
+// tie k + 1/2 is at least 1/512 away from one (255/512 is), so the sum with 192, which the one
 // rounding of the multiply-add takes to a multiple of 2^-16, restores the ties and
 // moves nothing across them.  The addition rounds to an integer: 1.5 2^23 + 8 - 192 +
 // the sum lies where fp32 has spacing 1.

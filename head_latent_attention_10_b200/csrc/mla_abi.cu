@@ -355,8 +355,9 @@ mla_status_t run_tc_decode(const mla_dims_t *dims, const void *q_abs, const void
 }
 
 // Ranges (persistent CTAs per row group) of the 4-bit decode on the current
-// device: one CTA per SM, fewer where the table holds so few pages that a
-// range would get less than kD4MinTiles of them.
+// device: one CTA per SM, fewer where the table holds less than kD4MinTiles pages
+// for each.  (The ranges are equal in plan_range's cost, which counts four tiles for a
+// sequence's start: of a short sequence's ranges the first may hold no tile.)
 int decode_int4_ranges(int groups, int B, int max_blocks)
 {
     const int sms = sm_count();

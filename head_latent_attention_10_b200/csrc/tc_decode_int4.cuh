@@ -12,8 +12,9 @@
 //
 // What bounds it: an M=64 MMA runs at half the tensor pipe's rate, 1,154 + 1,012
 // cycles of pipe work per page and 64 rows, which at 128 heads is far above the
-// page's 20,736 bytes; a full-rate M=128 would need O for 128 rows, all of
-// TMEM.  So the kernel is built to keep that pipe fed:
+// page's 20,736 bytes; a full-rate M=128 needs O for 128 rows, all of one SM's TMEM
+// (64 rows in each CTA of a cta_group::2 pair, with Q in shared memory, would fit: not
+// built).  So the kernel is built to keep that pipe fed:
 //   - One elected thread issues every MMA (warp 1), in the order S(k+1), P C(k),
 //     S(k+2), ...: between S(k)'s end and P C(k)'s start the pipe has 2,166
 //     cycles of other work, and the same between the release of a page's stage
@@ -73,7 +74,7 @@ constexpr int kD4OffList = kD4OffEpi + 4 * 16 * 128;
 constexpr int kD4List = 16;                       // published tile entries
 constexpr int kD4OffBar = kD4OffList + kD4List * 16;
 constexpr int kD4Smem = kD4OffBar + 256 + 1024;   // + alignment slack
-constexpr int kD4MinTiles = 2;                    // tiles of a range, where there are enough
+constexpr int kD4MinTiles = 2;                    // pages of the table a range, where there are few
 constexpr int kD4Ahead = 6;                       // tiles published ahead of the one being widened
 constexpr uint32_t kD4TmO = 16u << 16, kD4TmQ = 128;
 

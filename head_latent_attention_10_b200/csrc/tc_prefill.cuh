@@ -177,8 +177,9 @@ tc_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs a)
     const uint32_t tmem = *tmem_slot;
     const unsigned long long lim = a.limit_ns;
     const unsigned long long drain = lim > 200000000ull ? lim : 200000000ull;
-    // launched with programmatic serialization: the set-up above overlaps the end of
-    // the expansions, whose outputs are read only from here on
+    // launched with programmatic serialization: the expansions' outputs are read only
+    // from here on.  (They hold no trigger, so this kernel starts when their last CTAs
+    // exit: its launch overlaps them, its set-up hardly.)
     sm100::pdl_wait();
 
     // An item: 128 queries of one head of one sequence; within a head the longest rows

@@ -88,7 +88,8 @@ typedef enum {
                                   by the combine kernel, none inside the
                                   decode kernel; the results are the same bits
                                   either way (the two merges take the same
-                                  steps in the same order). */
+                                  steps in the same order).  mla_decode_int4
+                                  merges so without it. */
 
 typedef struct {
     int32_t num_heads;   /* H */
