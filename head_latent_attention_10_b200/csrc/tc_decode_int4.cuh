@@ -47,8 +47,8 @@
 // Rows past a sequence's end get logit -inf, so weight 0; any pattern a page
 // can hold is finite, so their latents add exactly 0 and need no zeroing.
 //
-// Measured (call, back to back): 128 sequences x 128 heads x 4,096 tokens 203 us (146
-// GFLOP: 88 us at the pipe's full rate, 126 us at M=64; the pipe is active in 70 % of
+// Measured (call, back to back): 128 sequences x 128 heads x 4,096 tokens 203 to 213 us
+// by box (146 GFLOP: 88 us at the pipe's full rate, 126 us at M=64; the pipe is active in 70 % of
 // the cycles), 64 x 16 heads x 4,096 62 us (87 MB: 13 us), one sequence of 16 heads
 // and 256 tokens 15 us.  A tile takes about 2,700 cycles: its 2,166 of MMAs and gaps
 // before each group of them.  A sequence's end inside a range takes about 14,000
